@@ -495,7 +495,7 @@ def _run_own(s):
     q = s["q"]
     B, hq, Tq, d = q.shape
     if op == "select":
-        idx = torch.zeros((B, Tq, s["k"].shape[1], s["cap"]), dtype=torch.int32, device=q.device)
+        idx = torch.empty((B, Tq, s["k"].shape[1], s["cap"]), dtype=torch.int32, device=q.device)
         cnt = torch.empty(idx.shape[:3], dtype=torch.int32, device=q.device)
         svsa.svsa_cache_select(c, q, idx, cnt, svsa.cache_query(q, causal=s["causal"], cap=s["cap"], first=s["first"], last=s["last"]))
         return {"idx": idx, "cnt": cnt}

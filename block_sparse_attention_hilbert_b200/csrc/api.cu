@@ -11,6 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "stream.cuh"
 #include "svsa.h"
 
 namespace svsa {
@@ -88,6 +89,22 @@ cudaError_t launch_check_pairs(const int32_t* pairs, long long BH, int nb, cudaS
 cudaError_t sics_flags(unsigned int* v, cudaStream_t st);
 cudaError_t reorder_flags(unsigned int* v, cudaStream_t st);
 cudaError_t pool_flags(unsigned int* v, cudaStream_t st);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, int f16, cudaStream_t st);
+size_t norm_rope_bwd_workspace_bytes(const NormRopeArgs& a, int d);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, int d, int f16, float* dwq, float* dwk, cudaStream_t st);
+cudaError_t rope_flags(unsigned int* v, cudaStream_t st);
+cudaError_t launch_cache_append(const CacheArgs& c, const void* k, const void* v, const long long k_stride[3],
+                                const long long v_stride[3], const int32_t* n_new, int32_t* len_out, int N, int f16,
+                                cudaStream_t st);
+cudaError_t launch_cache_select(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal, int cap,
+                                int first, int last, int32_t* idx, int32_t* cnt, cudaStream_t st);
+cudaError_t cache_flags(unsigned int* v, cudaStream_t st);
+size_t cache_attn_workspace_bytes(int d);
+cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal,
+                              const int32_t* idx, const int32_t* cnt, int cap, void* o, float* lse, void* ws,
+                              cudaStream_t st);
+cudaError_t cattn_flags(unsigned int* v, cudaStream_t st);
+cudaError_t cattn_error(unsigned int* code, cudaStream_t st);
 svsa_status record_error(svsa_status st, const char* msg);
 }  // namespace svsa
 
@@ -861,6 +878,295 @@ svsa_status svsa_selftest_timeout(int32_t wait_us, void* stream) {
                      "selftest launch");
 }
 
+// ---- streaming entry points -------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+svsa_status check_strides(const int64_t stride[3], const char* name) {
+  for (int e = 0; e < 3; ++e) {
+    if (stride[e] < 0 || stride[e] % 8 != 0)
+      return fail(SVSA_ERR_INVALID_ARG, "%s[%d]=%lld must be a multiple of 8, >= 0", name, e, (long long)stride[e]);
+    if (stride[e] > (1LL << 40)) return fail(SVSA_ERR_UNSUPPORTED, "%s[%d]=%lld", name, e, (long long)stride[e]);
+  }
+  return SVSA_OK;
+}
+
+// Rows of d values at sizes x strides must not overlap (they are written).
+svsa_status check_apart(const int32_t size[3], const int64_t stride[3], int d, const char* name) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+  int64_t extent = d;
+  for (int i = 0; i < 3; ++i) {
+    const int e = order[i];
+    if (size[e] <= 1) continue;
+    if (stride[e] < extent)
+      return fail(SVSA_ERR_INVALID_ARG, "%s: rows overlap (stride %lld < %lld), so the gradients would", name,
+                  (long long)stride[e], (long long)extent);
+    extent += stride[e] * (size[e] - 1);
+  }
+  return SVSA_OK;
+}
+
+svsa_status rope_args(const svsa_norm_rope* p, NormRopeArgs* a) {
+  if (p == nullptr) return fail(SVSA_ERR_INVALID_ARG, "params is NULL");
+  if (p->B < 1 || p->N < 1 || p->rows < 1 || p->heads_q < 1 || p->heads_k < 0)
+    return fail(SVSA_ERR_INVALID_ARG, "B, N, rows and heads_q must be >= 1, heads_k >= 0");
+  if (p->d != 64 && p->d != 128) return fail(SVSA_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", p->d);
+  if (p->dtype != SVSA_BF16 && p->dtype != SVSA_F16) return fail(SVSA_ERR_UNSUPPORTED, "dtype=%d unknown", p->dtype);
+  if (p->pairing != SVSA_PAIR_ADJACENT && p->pairing != SVSA_PAIR_HALVES)
+    return fail(SVSA_ERR_INVALID_ARG, "pairing=%d unknown", p->pairing);
+  if (!(p->eps >= 0.f)) return fail(SVSA_ERR_INVALID_ARG, "eps=%g must be >= 0", (double)p->eps);
+  if (p->axes < 0 || p->axes > 3) return fail(SVSA_ERR_INVALID_ARG, "axes=%d must be in [0, 3]", p->axes);
+  *a = NormRopeArgs{};
+  if (p->axes > 0) {
+    int sum = 0;
+    for (int e = 0; e < p->axes; ++e) {
+      if (p->pairs[e] < 0 || p->pairs[e] > p->d / 2) return fail(SVSA_ERR_INVALID_ARG, "pairs[%d]=%d", e, p->pairs[e]);
+      sum += p->pairs[e];
+    }
+    if (sum != p->d / 2) return fail(SVSA_ERR_INVALID_ARG, "the axes' pairs sum to %d, not d/2 = %d", sum, p->d / 2);
+    if (p->table_rows < 1) return fail(SVSA_ERR_INVALID_ARG, "table_rows=%d must be >= 1", p->table_rows);
+    if (p->pos_stride < 0) return fail(SVSA_ERR_INVALID_ARG, "pos_stride must be >= 0");
+    a->split1 = p->pairs[0];
+    a->split2 = p->axes > 1 ? p->pairs[0] + p->pairs[1] : p->d / 2;
+  }
+  SVSA_TRY(check_strides(p->q_stride, "q_stride"));
+  if (p->heads_k > 0) SVSA_TRY(check_strides(p->k_stride, "k_stride"));
+  // lane groups of one launch: at most one per (row, head)
+  if ((long long)p->B * std::max(p->rows, p->N) >= (1LL << 31) ||
+      (long long)p->B * std::max(p->rows, p->N) * ((long long)p->heads_q + p->heads_k) >= (1LL << 34))
+    return fail(SVSA_ERR_UNSUPPORTED, "too many rows for one call");
+  a->heads[0] = p->heads_q;
+  a->heads[1] = p->heads_k;
+  a->B = p->B;
+  a->N = p->N;
+  a->rows = p->rows;
+  a->axes = p->axes;
+  a->table_rows = p->table_rows;
+  a->halves = p->pairing;
+  a->eps = p->eps;
+  a->pos_stride = p->pos_stride;
+  for (int e = 0; e < 3; ++e) {
+    a->stride[0][e] = p->q_stride[e];
+    a->stride[1][e] = p->k_stride[e];
+    a->out_stride[0][e] = p->dq_stride[e];
+    a->out_stride[1][e] = p->dk_stride[e];
+  }
+  return SVSA_OK;
+}
+
+// The inputs that the forward and the backward share.
+svsa_status rope_inputs(const svsa_norm_rope* p, NormRopeArgs* a, const void* q, const void* k, const float* wq,
+                        const float* wk, const float* cos, const float* sin, const int32_t* pos, const int32_t* map,
+                        const char* map_name) {
+  SVSA_PTR(q, "q");
+  a->x[0] = q;
+  a->w[0] = wq;
+  if (wq) SVSA_PTR(wq, "wq");
+  if (p->heads_k > 0) {
+    SVSA_PTR(k, "k");
+    if (wk) SVSA_PTR(wk, "wk");
+    a->x[1] = k;
+    a->w[1] = wk;
+  }
+  if (p->axes > 0) {
+    SVSA_PTR(cos, "cos");
+    SVSA_PTR(sin, "sin");
+    SVSA_PTR(pos, "pos");
+    a->cos = cos;
+    a->sin = sin;
+    a->pos = pos;
+  }
+  if (map) SVSA_PTR(map, map_name);
+  else if (p->rows != p->N) return fail(SVSA_ERR_INVALID_ARG, "rows=%d without a map must be N=%d", p->rows, p->N);
+  a->map = map;
+  return SVSA_OK;
+}
+
+svsa_status cache_args(const svsa_cache* c, bool need_mean, CacheArgs* a) {
+  if (c == nullptr) return fail(SVSA_ERR_INVALID_ARG, "cache is NULL");
+  if (c->B < 1 || c->heads < 1 || c->n_pages < 1 || c->max_blocks < 1)
+    return fail(SVSA_ERR_INVALID_ARG, "B, heads, n_pages and max_blocks must be >= 1");
+  if (c->d != 64 && c->d != 128) return fail(SVSA_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", c->d);
+  if (c->code != SVSA_CODE_E4M3 && c->code != SVSA_CODE_I8) return fail(SVSA_ERR_UNSUPPORTED, "code=%d unknown", c->code);
+  if ((long long)c->n_pages * c->heads >= (1LL << 25))
+    return fail(SVSA_ERR_UNSUPPORTED, "n_pages * heads = %lld exceeds 2^25", (long long)c->n_pages * c->heads);
+  if (c->max_blocks > (1 << 24)) return fail(SVSA_ERR_UNSUPPORTED, "max_blocks=%d exceeds 2^24", c->max_blocks);
+  SVSA_PTR(c->k, "cache.k");
+  SVSA_PTR(c->v, "cache.v");
+  SVSA_PTR(c->k_scale, "cache.k_scale");
+  SVSA_PTR(c->v_scale, "cache.v_scale");
+  SVSA_PTR(c->table, "cache.table");
+  SVSA_PTR(c->len, "cache.len");
+  if (need_mean || c->mean != nullptr || c->mean_scale != nullptr) {
+    SVSA_PTR(c->mean, "cache.mean");
+    SVSA_PTR(c->mean_scale, "cache.mean_scale");
+  }
+  *a = CacheArgs{c->k, c->v, c->k_scale, c->v_scale, c->mean, c->mean_scale, c->table, c->len,
+                 c->B, c->heads, c->d, c->code == SVSA_CODE_I8, c->n_pages, c->max_blocks};
+  return SVSA_OK;
+}
+
+svsa_status check_query(const svsa_cache* c, const svsa_cache_query* p) {
+  if (p == nullptr) return fail(SVSA_ERR_INVALID_ARG, "params is NULL");
+  if (p->Tq < 1 || p->heads_q < 1 || p->heads_q % c->heads != 0)
+    return fail(SVSA_ERR_INVALID_ARG, "Tq=%d must be >= 1, heads_q=%d a multiple of %d", p->Tq, p->heads_q, c->heads);
+  if (p->dtype != SVSA_BF16 && p->dtype != SVSA_F16) return fail(SVSA_ERR_UNSUPPORTED, "dtype=%d unknown", p->dtype);
+  if (p->causal != 0 && p->causal != 1) return fail(SVSA_ERR_INVALID_ARG, "causal=%d must be 0 or 1", p->causal);
+  if ((long long)c->B * p->heads_q * p->Tq >= (1LL << 27))
+    return fail(SVSA_ERR_UNSUPPORTED, "B*heads_q*Tq = %lld exceeds 2^27", (long long)c->B * p->heads_q * p->Tq);
+  return SVSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+svsa_status svsa_qk_norm_rope(const void* q, const void* k, const float* wq, const float* wk, const float* cos,
+                              const float* sin, const int32_t* pos, const int32_t* map, void* yq, void* yk,
+                              const svsa_norm_rope* p, void* stream) {
+  NvtxRange nvtx_("svsa_qk_norm_rope");
+  g_last_error.clear();
+  NormRopeArgs a;
+  SVSA_TRY(rope_args(p, &a));
+  SVSA_TRY(rope_inputs(p, &a, q, k, wq, wk, cos, sin, pos, map, "map"));
+  SVSA_PTR(yq, "yq");
+  if (p->heads_k > 0) SVSA_PTR(yk, "yk");
+  if (yq == q || (p->heads_k > 0 && (yk == k || yk == q || yq == k || yq == yk)))
+    return fail(SVSA_ERR_INVALID_ARG, "input and output must not alias");
+  a.out[0] = yq;
+  a.out[1] = yk;
+  return cuda_status(counted(launch_norm_rope(a, p->d, p->dtype == SVSA_F16, (cudaStream_t)stream), 1),
+                     "qk_norm_rope launch");
+}
+
+size_t svsa_qk_norm_rope_bwd_workspace_bytes(const svsa_norm_rope* p) {
+  NormRopeArgs a;
+  if (rope_args(p, &a) != SVSA_OK) return 0;
+  return norm_rope_bwd_workspace_bytes(a, p->d);
+}
+
+svsa_status svsa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* q, const void* k, const float* wq,
+                                  const float* wk, const float* cos, const float* sin, const int32_t* pos,
+                                  const int32_t* imap, void* dq, void* dk, float* dwq, float* dwk,
+                                  const svsa_norm_rope* p, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("svsa_qk_norm_rope_bwd");
+  g_last_error.clear();
+  NormRopeArgs a;
+  SVSA_TRY(rope_args(p, &a));
+  SVSA_TRY(rope_inputs(p, &a, q, k, wq, wk, cos, sin, pos, imap, "imap"));
+  const int32_t qs[3] = {p->B, p->heads_q, p->N}, ks[3] = {p->B, p->heads_k, p->N};
+  SVSA_TRY(check_strides(p->dq_stride, "dq_stride"));
+  SVSA_TRY(check_apart(qs, p->dq_stride, p->d, "dq_stride"));
+  SVSA_PTR(dyq, "dyq");
+  SVSA_PTR(dq, "dq");
+  a.dy[0] = dyq;
+  a.out[0] = dq;
+  if (p->heads_k > 0) {
+    SVSA_TRY(check_strides(p->dk_stride, "dk_stride"));
+    SVSA_TRY(check_apart(ks, p->dk_stride, p->d, "dk_stride"));
+    SVSA_PTR(dyk, "dyk");
+    SVSA_PTR(dk, "dk");
+    a.dy[1] = dyk;
+    a.out[1] = dk;
+  }
+  if (dq == dyq || dq == q || (p->heads_k > 0 && (dk == dyk || dk == k || dk == dq || dk == dyq || dq == dyk)))
+    return fail(SVSA_ERR_INVALID_ARG, "input and output must not alias");
+  if (dwq) SVSA_PTR(dwq, "dwq");
+  if (dwk && p->heads_k > 0) SVSA_PTR(dwk, "dwk");
+  const size_t need = norm_rope_bwd_workspace_bytes(a, p->d);
+  SVSA_PTR(ws, "ws");
+  if (ws_bytes < need) return fail(SVSA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  a.part = static_cast<float*>(ws);
+  float* const wk_out = p->heads_k > 0 ? dwk : nullptr;
+  return cuda_status(counted(launch_norm_rope_bwd(a, p->d, p->dtype == SVSA_F16, dwq, wk_out, (cudaStream_t)stream),
+                             dwq || wk_out ? 2 : 1),
+                     "qk_norm_rope_bwd launch");
+}
+
+svsa_status svsa_cache_append(const svsa_cache* c, const void* k, const void* v, const int32_t* n_new,
+                              int32_t* len_out, const svsa_cache_tokens* p, void* stream) {
+  NvtxRange nvtx_("svsa_cache_append");
+  g_last_error.clear();
+  CacheArgs a;
+  SVSA_TRY(cache_args(c, false, &a));
+  if (p == nullptr) return fail(SVSA_ERR_INVALID_ARG, "params is NULL");
+  if (p->N < 1) return fail(SVSA_ERR_INVALID_ARG, "N=%d must be >= 1", p->N);
+  if (p->dtype != SVSA_BF16 && p->dtype != SVSA_F16) return fail(SVSA_ERR_UNSUPPORTED, "dtype=%d unknown", p->dtype);
+  SVSA_TRY(check_strides(p->k_stride, "k_stride"));
+  SVSA_TRY(check_strides(p->v_stride, "v_stride"));
+  if (((long long)p->N / kBlock + 2) * c->heads * c->B >= (1LL << 31))
+    return fail(SVSA_ERR_UNSUPPORTED, "too many blocks for one call");
+  SVSA_PTR(k, "k");
+  SVSA_PTR(v, "v");
+  if (n_new) SVSA_PTR(n_new, "n_new");
+  if (len_out) SVSA_PTR(len_out, "len_out");
+  if (len_out == c->len || (n_new && len_out == n_new))
+    return fail(SVSA_ERR_INVALID_ARG, "len_out must not alias len or n_new");
+  if (c->k == c->v || c->k_scale == c->v_scale)
+    return fail(SVSA_ERR_INVALID_ARG, "keys and values must have codes and scales of their own");
+  long long ks[3], vs[3];
+  for (int e = 0; e < 3; ++e) {
+    ks[e] = p->k_stride[e];
+    vs[e] = p->v_stride[e];
+  }
+  return cuda_status(counted(launch_cache_append(a, k, v, ks, vs, n_new, len_out, p->N, p->dtype == SVSA_F16,
+                                                 (cudaStream_t)stream), 1),
+                     "cache_append launch");
+}
+
+svsa_status svsa_cache_select(const svsa_cache* c, const void* q, int32_t* idx, int32_t* cnt,
+                              const svsa_cache_query* p, void* stream) {
+  NvtxRange nvtx_("svsa_cache_select");
+  g_last_error.clear();
+  CacheArgs a;
+  SVSA_TRY(cache_args(c, true, &a));
+  SVSA_TRY(check_query(c, p));
+  if (p->cap < 1 || p->first < 0 || p->last < 0 || (long long)p->first + p->last > p->cap)
+    return fail(SVSA_ERR_INVALID_ARG, "cap=%d must be >= 1 and hold first=%d and last=%d", p->cap, p->first, p->last);
+  if (c->max_blocks > 65536) return fail(SVSA_ERR_UNSUPPORTED, "max_blocks=%d exceeds 65536", c->max_blocks);
+  if (p->heads_q / c->heads > 128)
+    return fail(SVSA_ERR_UNSUPPORTED, "%d query heads per key head exceed 128", p->heads_q / c->heads);
+  SVSA_PTR(q, "q");
+  SVSA_PTR(idx, "idx");
+  SVSA_PTR(cnt, "cnt");
+  return cuda_status(counted(launch_cache_select(a, q, p->heads_q, p->Tq, p->dtype == SVSA_F16, p->causal, p->cap,
+                                                 p->first, p->last, idx, cnt, (cudaStream_t)stream), 1),
+                     "cache_select launch");
+}
+
+size_t svsa_cache_attn_workspace_bytes(const svsa_cache* c, const svsa_cache_query* p) {
+  if (c == nullptr || p == nullptr || (c->d != 64 && c->d != 128)) return 0;
+  return cache_attn_workspace_bytes(c->d);
+}
+
+svsa_status svsa_cache_attn(const svsa_cache* c, const void* q, const int32_t* idx, const int32_t* cnt, void* o,
+                            float* lse, const svsa_cache_query* p, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("svsa_cache_attn");
+  g_last_error.clear();
+  CacheArgs a;
+  SVSA_TRY(cache_args(c, false, &a));
+  SVSA_TRY(check_query(c, p));
+  SVSA_PTR(q, "q");
+  SVSA_PTR(o, "o");
+  if (q == o) return fail(SVSA_ERR_INVALID_ARG, "input and output must not alias");
+  if (lse) SVSA_PTR(lse, "lse");
+  if ((idx == nullptr) != (cnt == nullptr)) return fail(SVSA_ERR_INVALID_ARG, "idx and cnt go together");
+  if (idx) {
+    SVSA_PTR(idx, "idx");
+    SVSA_PTR(cnt, "cnt");
+    if (p->cap < 1 || p->cap > (1 << 24)) return fail(SVSA_ERR_INVALID_ARG, "cap=%d must be in [1, 2^24]", p->cap);
+  }
+  const size_t need = cache_attn_workspace_bytes(c->d);
+  SVSA_PTR(ws, "ws");
+  if (ws_bytes < need) return fail(SVSA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  return cuda_status(counted(launch_cache_attn(a, q, p->heads_q, p->Tq, p->dtype == SVSA_F16, p->causal, idx, cnt,
+                                               p->cap, o, lse, ws, (cudaStream_t)stream), 2),
+                     "cache_attn launch");
+}
+
 svsa_status svsa_sync_status(void* stream) {
   NvtxRange nvtx_("svsa_sync_status");
   g_last_error.clear();
@@ -869,12 +1175,12 @@ svsa_status svsa_sync_status(void* stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e, "asynchronous error");
   // every tensor-core translation unit keeps its own error word; read (and clear) all of them
-  cudaError_t (*readers[5])(unsigned int*, cudaStream_t) = {attn_fa_error, attn_tc_error, scores_tc_error,
-                                                           route_tc_error, cocluster_tc_error};
-  const char* names[5] = {"attention", "self-test", "scores", "routing", "co-clustering"};
+  cudaError_t (*readers[6])(unsigned int*, cudaStream_t) = {attn_fa_error, attn_tc_error, scores_tc_error,
+                                                           route_tc_error, cocluster_tc_error, cattn_error};
+  const char* names[6] = {"attention", "self-test", "scores", "routing", "co-clustering", "cache attention"};
   unsigned int first_code = 0u;
   const char* first_name = nullptr;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 6; ++i) {
     unsigned int code = 0u;
     e = readers[i](&code, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_status(e, "reading the device error word");
@@ -884,19 +1190,25 @@ svsa_status svsa_sync_status(void* stream) {
     }
   }
   // status bits of the data checks (reading clears them)
-  unsigned int fl[3] = {0u, 0u, 0u};
-  cudaError_t (*flag_readers[3])(unsigned int*, cudaStream_t) = {reorder_flags, pool_flags, sics_flags};
-  for (int i = 0; i < 3; ++i) {
+  unsigned int fl[6] = {0u, 0u, 0u, 0u, 0u, 0u};
+  cudaError_t (*flag_readers[6])(unsigned int*, cudaStream_t) = {reorder_flags, pool_flags, sics_flags,
+                                                                 rope_flags, cache_flags, cattn_flags};
+  for (int i = 0; i < 6; ++i) {
     e = flag_readers[i](&fl[i], (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_status(e, "reading a status word");
   }
-  const unsigned int bits = fl[0] | fl[1] | fl[2];
+  const unsigned int bits = fl[0] | fl[1] | fl[2] | fl[3] | fl[4] | fl[5];
   if (first_name != nullptr)
     return fail(SVSA_ERR_TIMEOUT, "%s kernel: a bounded wait gave up (site %u)", first_name, first_code);
   if (bits & kFlagMask)
     return fail(SVSA_ERR_MASK, "a mask list checked before the attention was malformed "
                                "(kv_cnt outside [0, cap], an index outside [0, nb), not strictly ascending, "
                                "or a pairing table that is not a permutation)");
+  if (bits & kFlagIndex)
+    return fail(SVSA_ERR_INDEX, "a position, token map entry, page, length or list entry lay outside its range; "
+                                "it was clamped or left out");
+  if (bits & kFlagNotFinite)
+    return fail(SVSA_ERR_RANGE, "a value that is not finite was given to an 8-bit conversion; the result saturated");
   if (bits & (kFlagRangeValue | kFlagRangeMean))
     return fail(SVSA_ERR_RANGE, "%s beyond the fp16 range (+-65504) or not finite; the result saturated",
                 (bits & kFlagRangeValue) ? "a value given to svsa_reorder_values" : "a block mean of the scores");

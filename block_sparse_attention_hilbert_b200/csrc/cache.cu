@@ -1,0 +1,540 @@
+// The 8-bit block cache: appending tokens, and choosing blocks for queries.
+//
+// cache_append_kernel  one CTA per (sequence, head, block that receives
+//   tokens).  For K and V: amax of the new rows, the block's scale = the
+//   larger of what it had and the smallest power of two that holds amax; the
+//   codes of rows that were there are rounded again only when the scale grew.
+//   Then the block's key mean from the codes: in units of the code's last
+//   place (1 for int8, 2^-9 for e4m3) the column sums are whole numbers below
+//   2^24, so the mean does not depend on the order of the sum.
+//   Bound by HBM for long appends (4 bytes read and 2 written per key and
+//   value pair, in 16- and 8-byte pieces), by launch latency for one token.
+//
+// cache_select_kernel  one cluster of CTAs per (sequence, query, key head).
+//   score(block) = max over the group's query heads of q . mean(block), both
+//   in 8 bits with power-of-two scales: an integer dot product below 2^21
+//   times a power of two, exact in fp32, so that no list depends on the order
+//   of a sum and equal scores are really equal (the lower index wins).  Each
+//   CTA scores a range of blocks, one thread per block (its mean is one
+//   128-byte line), and keeps the sortable keys in shared memory; the cap-th
+//   largest key is found by four 8-bit digits with histograms summed over
+//   the cluster, and the list is written in ascending order.
+#include <cooperative_groups.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "stream.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace svsa {
+
+static __device__ unsigned int g_cache_flags;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+template <typename T>
+__device__ __forceinline__ void unpack8(uint4 v, float x[8]);
+template <>
+__device__ __forceinline__ void unpack8<__nv_bfloat16>(uint4 v, float x[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void unpack8<__half>(uint4 v, float x[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// The code of y = x / scale, rounded to nearest even and saturated; NaN gives 0.
+template <bool I8>
+__device__ __forceinline__ uint32_t encode(float y) {
+  if (y != y) return 0u;
+  if constexpr (I8) {
+    const int c = __float2int_rn(fminf(fmaxf(y, -127.f), 127.f));
+    return (uint32_t)c & 0xffu;
+  } else {
+    return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
+// A code as a whole number of its last places: int8 itself; e4m3 in units of
+// 2^-9, (m or 8 + m) << (e - 1), below 2^18.
+template <bool I8>
+__device__ __forceinline__ int decode_units(uint32_t c) {
+  if constexpr (I8) {
+    return (int)(int8_t)c;
+  } else {
+    const int e = (c >> 3) & 15, m = c & 7;
+    const int v = e ? (8 + m) << (e - 1) : m;
+    return (c & 0x80u) ? -v : v;
+  }
+}
+
+template <bool I8>
+constexpr float unit() { return I8 ? 1.f : 1.f / 512.f; }
+
+struct AppendArgs {
+  CacheArgs c;
+  const void* x[2];                // k, v
+  long long stride[2][3];          // batch, head, token
+  const int32_t* n_new;            // nullable
+  int32_t* len_out;                // nullable
+  int N, wide;                     // wide: blocks that N tokens can touch
+};
+
+template <int D, typename T, bool I8>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendArgs p) {
+  constexpr int L = D / 8;                 // lanes per row
+  constexpr int R = kThreads / L;          // rows per pass
+  constexpr int P = kBlock / R;            // passes: 4 (d = 128) or 2 (d = 64)
+  __shared__ float wmax[2][kWarps];
+  __shared__ int sums[R][D];
+  const int ch = threadIdx.x % L, rl = threadIdx.x / L;
+  long long blk_id = blockIdx.x;
+  const int x = (int)(blk_id % p.wide);
+  blk_id /= p.wide;
+  const int h = (int)(blk_id % p.c.heads), b = (int)(blk_id / p.c.heads);
+
+  const int room = p.c.max_blocks * kBlock;
+  const int len0 = __ldg(p.c.len + b), new0 = p.n_new ? __ldg(p.n_new + b) : p.N;
+  const int len = min(max(len0, 0), room);
+  const int n_new = min(min(max(new0, 0), p.N), room - len);
+  if (x == 0 && h == 0 && threadIdx.x == 0) {
+    if (len != len0 || n_new != new0) atomicOr(&g_cache_flags, kFlagIndex);
+    if (p.len_out) p.len_out[b] = len + n_new;
+  }
+  const int j = len / kBlock + x;                      // block of the sequence
+  const int lo = max(len, j * kBlock), hi = min(len + n_new, (j + 1) * kBlock);
+  if (lo >= hi) return;
+  const int page = __ldg(p.c.table + (long long)b * p.c.max_blocks + j);
+  if ((unsigned)page >= (unsigned)p.c.n_pages) {
+    if (threadIdx.x == 0) atomicOr(&g_cache_flags, kFlagIndex);
+    return;
+  }
+  const int had = lo - j * kBlock, end = hi - j * kBlock;   // rows [had, end) of the block are new
+  const long long cell = (long long)page * p.c.heads + h;
+  uint8_t* codes[2] = {static_cast<uint8_t*>(p.c.k) + cell * (kBlock * D), static_cast<uint8_t*>(p.c.v) + cell * (kBlock * D)};
+  float* scales[2] = {p.c.k_scale + cell, p.c.v_scale + cell};
+
+  uint4 raw[2][P];
+  float amax[2] = {0.f, 0.f};
+  bool odd = false;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const char* src = static_cast<const char*>(p.x[w]) +
+                      2 * ((long long)b * p.stride[w][0] + (long long)h * p.stride[w][1]) + ch * 16;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int r = rl + R * i;
+      raw[w][i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= had && r < end)
+        raw[w][i] = *reinterpret_cast<const uint4*>(src + 2 * (long long)(j * kBlock + r - len) * p.stride[w][2]);
+    }
+  }
+  float start[2];
+  start[0] = had > 0 ? *scales[0] : 0.f;
+  start[1] = had > 0 ? *scales[1] : 0.f;
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float v[8];
+      unpack8<T>(raw[w][i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(v[e]);
+        if (a < INFINITY) amax[w] = fmaxf(amax[w], a);
+        else odd = true;
+      }
+    }
+  if (odd) atomicOr(&g_cache_flags, kFlagNotFinite);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    amax[w] = warp_max(amax[w]);
+    if (threadIdx.x % 32 == 0) wmax[w][threadIdx.x / 32] = amax[w];
+  }
+  __syncthreads();                                     // also: every thread has read the old scales
+  float scale[2], inv[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float m = wmax[w][0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) m = fmaxf(m, wmax[w][i]);
+    scale[w] = fmaxf(start[w], pow2_scale(m, I8));
+    inv[w] = scale[w] > 0.f ? 1.f / scale[w] : 0.f;
+  }
+  if (threadIdx.x < 2) *scales[threadIdx.x] = threadIdx.x ? scale[1] : scale[0];
+
+  int total[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const bool grew = had > 0 && scale[w] != start[w];
+    const float back = grew ? start[w] / scale[w] : 1.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int r = rl + R * i;
+      uint2* at = reinterpret_cast<uint2*>(codes[w] + (long long)r * D + ch * 8);
+      uint32_t c[2] = {0u, 0u};
+      if (r >= had && r < end) {
+        float v[8];
+        unpack8<T>(raw[w][i], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e / 4] |= encode<I8>(v[e] * inv[w]) << (8 * (e % 4));
+        *at = make_uint2(c[0], c[1]);
+      } else if (r < had && (grew || w == 0)) {
+        const uint2 old = *at;
+        c[0] = old.x;
+        c[1] = old.y;
+        if (grew) {
+          uint32_t n[2] = {0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t was = (c[e / 4] >> (8 * (e % 4))) & 0xffu;
+            uint32_t now = encode<I8>((float)decode_units<I8>(was) * unit<I8>() * back);
+            if (!I8) now |= was & 0x80u;                    // -0 keeps its sign
+            n[e / 4] |= now << (8 * (e % 4));
+          }
+          c[0] = n[0];
+          c[1] = n[1];
+          *at = make_uint2(c[0], c[1]);
+        }
+      }
+      if (w == 0 && r < end) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) total[e] += decode_units<I8>((c[e / 4] >> (8 * (e % 4))) & 0xffu);
+      }
+    }
+  }
+  if (p.c.mean == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[rl][ch * 8 + e] = total[e];
+  __syncthreads();
+  float mean = 0.f;
+  if (threadIdx.x < D) {
+    int t = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) t += sums[r][threadIdx.x];
+    mean = __fdiv_rn((float)t, (float)end);
+  }
+  const float m = warp_max(fabsf(mean));
+  if (threadIdx.x < D && threadIdx.x % 32 == 0) wmax[1][threadIdx.x / 32] = m;    // (the barrier above parts it from the reads)
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float top = wmax[1][0];
+#pragma unroll
+    for (int i = 1; i < D / 32; ++i) top = fmaxf(top, wmax[1][i]);
+    const float s = pow2_scale(top, true);
+    p.c.mean[cell * D + threadIdx.x] = (int8_t)encode<true>(s > 0.f ? mean / s : 0.f);
+    if (threadIdx.x == 0) p.c.mean_scale[cell] = s * unit<I8>() * scale[0];
+  }
+}
+
+// ---------------------------------------------------------------- selection
+
+struct SelectArgs {
+  CacheArgs c;
+  const void* q;                   // [B][heads_q][Tq][d]
+  int32_t* idx;                    // [B][Tq][heads][cap]
+  int32_t* cnt;                    // [B][Tq][heads]
+  int heads_q, Tq, causal, cap, first, last;
+  int chunk;                       // blocks of a CTA at most
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) cache_select_kernel(const __grid_constant__ SelectArgs p) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ int hist[4][256];
+  __shared__ int found[2];
+  __shared__ int counts[2];        // keys above and at the threshold, read by the cluster
+  __shared__ int wsum[2][kWarps];
+  __shared__ int warp_tot[kWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int group = p.heads_q / p.c.heads;
+  uint32_t* keys = smem;                                   // [chunk]
+  uint32_t* qc = smem + (p.chunk + 3) / 4 * 4;             // [group][D / 4]
+  float* qs = reinterpret_cast<float*>(qc + group * (D / 4));
+
+  long long row = blockIdx.x / C;
+  const int h = (int)(row % p.c.heads);
+  row /= p.c.heads;
+  const int t = (int)(row % p.Tq), b = (int)(row / p.Tq);
+  const long long out_row = ((long long)b * p.Tq + t) * p.c.heads + h;
+  int32_t* idx = p.idx + out_row * p.cap;
+
+  const int len0 = __ldg(p.c.len + b);
+  const int len = min(max(len0, 0), p.c.max_blocks * kBlock);
+  const int seen = p.causal ? max(len - p.Tq + 1 + t, 0) : len;
+  const int nb = (seen + kBlock - 1) / kBlock;
+  if (rank == 0 && threadIdx.x == 0) {
+    p.cnt[out_row] = min(nb, p.cap);
+    if (len != len0) atomicOr(&g_cache_flags, kFlagIndex);
+  }
+  if (nb <= p.cap) {                                       // nothing to choose (uniform over the cluster)
+    for (int i = rank * kThreads + threadIdx.x; i < p.cap; i += C * kThreads) idx[i] = i < nb ? i : 0;
+    return;
+  }
+  const int per = (nb + C - 1) / C;
+  const int lo = min(rank * per, nb), n = min(lo + per, nb) - lo;
+
+  // the group's queries in 8 bits
+  for (int g = threadIdx.x / 32; g < group; g += kWarps) {
+    const T* q = static_cast<const T*>(p.q) + (((long long)b * p.heads_q + h * group + g) * p.Tq + t) * D;
+    const int lane = threadIdx.x % 32;
+    float v[D / 32];
+    float amax = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      v[e] = (float)q[lane * (D / 32) + e];
+      const float a = fabsf(v[e]);
+      if (a < INFINITY) amax = fmaxf(amax, a);
+      else odd = true;
+    }
+    if (odd) atomicOr(&g_cache_flags, kFlagNotFinite);
+    const float s = pow2_scale(warp_max(amax), true), inv = s > 0.f ? 1.f / s : 0.f;
+    uint32_t w = 0u;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) w |= encode<true>(v[e] * inv) << (8 * e);
+    if constexpr (D == 128) qc[g * (D / 4) + lane] = w;
+    else reinterpret_cast<uint16_t*>(qc + g * (D / 4))[lane] = (uint16_t)w;
+    if (lane == 0) qs[g] = s;
+  }
+  for (int i = threadIdx.x; i < 4 * 256; i += kThreads) hist[i / 256][i % 256] = 0;
+  __syncthreads();
+
+  bool bad = false;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int j = lo + i;
+    uint32_t key = 0u;
+    if (j < p.first || j >= nb - p.last) {
+      key = 0xffffffffu;
+    } else {
+      const int page = __ldg(p.c.table + (long long)b * p.c.max_blocks + j);
+      if ((unsigned)page >= (unsigned)p.c.n_pages) {
+        bad = true;
+      } else {
+        const long long cell = (long long)page * p.c.heads + h;
+        const uint4* mp = reinterpret_cast<const uint4*>(p.c.mean + cell * D);
+        uint4 m[D / 16];
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) m[e] = __ldg(mp + e);
+        const float ms = __ldg(p.c.mean_scale + cell);
+        float best = -INFINITY;
+        for (int g = 0; g < group; ++g) {
+          const uint4* qg = reinterpret_cast<const uint4*>(qc + g * (D / 4));
+          int dot = 0;
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint4 a = qg[e];
+            dot = __dp4a((int)a.x, (int)m[e].x, dot);
+            dot = __dp4a((int)a.y, (int)m[e].y, dot);
+            dot = __dp4a((int)a.z, (int)m[e].z, dot);
+            dot = __dp4a((int)a.w, (int)m[e].w, dot);
+          }
+          best = fmaxf(best, (float)dot * (qs[g] * ms));
+        }
+        const uint32_t u = __float_as_uint(best + 0.f);     // -0 becomes +0
+        key = (u & 0x80000000u) ? ~u : u | 0x80000000u;
+      }
+    }
+    keys[i] = key;
+    atomicAdd(&hist[0][key >> 24], 1);
+  }
+  if (bad) atomicOr(&g_cache_flags, kFlagIndex);
+
+  // the cap-th largest key: four digits, each from the cluster's summed histogram
+  uint32_t prefix = 0u;
+  int need = p.cap;
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    if (pass > 0) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t key = keys[i];
+        if ((key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[pass][(key >> shift) & 255u], 1);
+      }
+    }
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+    // thread t holds bin 255 - t; an inclusive scan over the threads counts the keys from the top
+    const int bin = 255 - threadIdx.x;
+    int c = 0;
+    for (int r = 0; r < C; ++r) c += C > 1 ? cluster.map_shared_rank(&hist[pass][0], r)[bin] : hist[pass][bin];
+    int up = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, up, o);
+      if ((threadIdx.x & 31) >= o) up += v;
+    }
+    if ((threadIdx.x & 31) == 31) warp_tot[threadIdx.x / 32] = up;
+    __syncthreads();
+    for (int w = 0; w < (int)threadIdx.x / 32; ++w) up += warp_tot[w];
+    if (up >= need && up - c < need) {
+      found[0] = bin;
+      found[1] = need - (up - c);
+    }
+    __syncthreads();
+    prefix |= (uint32_t)found[0] << shift;
+    need = found[1];
+  }
+
+  // keys above the threshold, and the first `need` equal to it
+  int above = 0, equal = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    above += keys[i] > prefix;
+    equal += keys[i] == prefix;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (threadIdx.x % 32 == 0) {
+    wsum[0][threadIdx.x / 32] = above;
+    wsum[1][threadIdx.x / 32] = equal;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    int s = 0;
+    for (int w = 0; w < kWarps; ++w) s += wsum[threadIdx.x][w];
+    counts[threadIdx.x] = s;
+  }
+  if (C > 1) cluster.sync();
+  else __syncthreads();
+  int taken = 0, ties = 0;                                  // before this CTA's range
+  for (int r = 0; r < rank; ++r) {
+    const int* o = cluster.map_shared_rank(&counts[0], r);
+    taken += o[0];
+    ties += o[1];
+  }
+  if (C > 1) cluster.sync();                                // no CTA leaves while another reads its counts
+  taken += min(ties, need);
+  for (int base = 0; base < n; base += kThreads) {
+    const int i = base + threadIdx.x;
+    const uint32_t key = i < n ? keys[i] : 0u;
+    const bool eq = i < n && key == prefix, gt = i < n && key > prefix;
+    const unsigned lanes = (1u << (threadIdx.x & 31)) - 1u;
+    const unsigned beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) {
+      wsum[0][threadIdx.x / 32] = __popc(bgt);
+      wsum[1][threadIdx.x / 32] = __popc(beq);
+    }
+    __syncthreads();
+    int g0 = 0, e0 = 0, gall = 0, eall = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int a = wsum[0][w], e = wsum[1][w];
+      if (w < (int)threadIdx.x / 32) {
+        g0 += a;
+        e0 += e;
+      }
+      gall += a;
+      eall += e;
+    }
+    const int eq_before = ties + e0 + __popc(beq & lanes);
+    const int gt_before = g0 + __popc(bgt & lanes);
+    // `taken` counts what lies before this tile; ties of this tile that are taken
+    const int tile_ties_before = min(eq_before, need) - min(ties, need);
+    if (gt || (eq && eq_before < need)) idx[taken + gt_before + tile_ties_before] = lo + i;
+    taken += gall + min(ties + eall, need) - min(ties, need);
+    ties += eall;
+  }
+}
+
+template <typename F>
+void by_d_type(int d, int f16, F&& f) {
+  auto t = [&](auto D_) {
+    if (f16) f(D_, __half{});
+    else f(D_, __nv_bfloat16{});
+  };
+  if (d == 128) t(std::integral_constant<int, 128>{});
+  else t(std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheArgs& c, const void* k, const void* v, const long long k_stride[3],
+                                const long long v_stride[3], const int32_t* n_new, int32_t* len_out, int N, int f16,
+                                cudaStream_t st) {
+  AppendArgs p{};
+  p.c = c;
+  p.x[0] = k;
+  p.x[1] = v;
+  for (int e = 0; e < 3; ++e) {
+    p.stride[0][e] = k_stride[e];
+    p.stride[1][e] = v_stride[e];
+  }
+  p.n_new = n_new;
+  p.len_out = len_out;
+  p.N = N;
+  // N tokens touch at most ceil((N - 1) / 64) + 1 blocks, wherever they start
+  p.wide = (N + kBlock - 2) / kBlock + 1;
+  const unsigned grid = (unsigned)((long long)p.wide * c.heads * c.B);
+  by_d_type(c.d, f16, [&](auto D_, auto z) {
+    constexpr int D = decltype(D_)::value;
+    using T = decltype(z);
+    if (c.i8) cache_append_kernel<D, T, true><<<grid, kThreads, 0, st>>>(p);
+    else cache_append_kernel<D, T, false><<<grid, kThreads, 0, st>>>(p);
+  });
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_select(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal, int cap,
+                                int first, int last, int32_t* idx, int32_t* cnt, cudaStream_t st) {
+  SelectArgs p{};
+  p.c = c;
+  p.q = q;
+  p.idx = idx;
+  p.cnt = cnt;
+  p.heads_q = heads_q;
+  p.Tq = Tq;
+  p.causal = causal;
+  p.cap = cap;
+  p.first = first;
+  p.last = last;
+  const long long rows = (long long)c.B * Tq * c.heads;
+  // CTAs per row: more while a CTA keeps at least one block per thread and the
+  // grid stays within a few CTAs per SM; and enough for the keys to fit
+  int C = 1;
+  while (C < 8 && c.max_blocks > C * kThreads && rows * C < kNumSMs * 4) C *= 2;
+  while (C < 8 && ceil_div(c.max_blocks, C) > 16384) C *= 2;
+  p.chunk = ceil_div(c.max_blocks, C);
+  const int group = heads_q / c.heads;
+  const size_t smem = (size_t)((p.chunk + 3) / 4 * 4) * 4 + (size_t)group * (c.d + 4);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaSuccess;
+  by_d_type(c.d, f16, [&](auto D_, auto z) {
+    auto kernel = cache_select_kernel<decltype(D_)::value, decltype(z)>;
+    if (smem > 32768) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
+  });
+  return e;
+}
+
+cudaError_t cache_flags(unsigned int* v, cudaStream_t st) { return read_and_clear_flags(g_cache_flags, v, st); }
+
+}  // namespace svsa

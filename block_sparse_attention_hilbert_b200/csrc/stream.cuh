@@ -1,0 +1,71 @@
+// Argument blocks and small device helpers of the streaming entry points
+// (norm and rotation, 8-bit block cache, block selection, cache attention).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace svsa {
+
+// More status bits (see common.cuh): bit 3 = an index (position, map entry,
+// page, length or list entry) out of range, bit 4 = a value that is not finite
+// given to an 8-bit conversion.
+constexpr unsigned int kFlagIndex = 8u, kFlagNotFinite = 16u;
+
+struct NormRopeArgs {
+  const void* x[2];
+  const void* dy[2];
+  void* out[2];
+  const float* w[2];
+  const float* cos;
+  const float* sin;
+  const int32_t* pos;
+  const int32_t* map;
+  float* part;
+  long long stride[2][3];          // inputs
+  long long out_stride[2][3];      // backward: gradients of the inputs
+  long long pos_stride;
+  int heads[2];
+  int B, N, rows, axes, split1, split2, table_rows, halves;
+  float eps;
+};
+
+// The cache: [page][head][64 tokens][d] codes with a scale per (page, head),
+// and per sequence a row of the table of pages and a length.
+struct CacheArgs {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int8_t* mean;                  // nullable: [page][head][d] key means and their scales
+  float* mean_scale;
+  const int32_t* table;          // [B][max_blocks]
+  const int32_t* len;            // [B]
+  int B, heads, d, i8, n_pages, max_blocks;
+};
+
+// The smallest power of two s with amax / s <= top, top = 127 (int8) or 448
+// (e4m3); 0 for amax = 0.  In binary, amax = f * 2^e with f in [1, 2), and top
+// = t * 2^b with t = 127/64 (b = 6) or 1.75 (b = 8): s = 2^(e - b), one more
+// where f > t.  Powers of two make x / s exact, so the codes do not depend on
+// how the division is done, and a block whose scale grows keeps what its codes
+// stand for up to one more rounding.
+__device__ __forceinline__ float pow2_scale(float amax, bool i8) {
+  if (!(amax > 0.f)) return 0.f;
+  uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127;
+  if (e == -127) {                                  // a subnormal: shift it up first
+    u = __float_as_uint(amax * 16777216.f);
+    e = (int)(u >> 23) - 127 - 24;
+  }
+  const uint32_t frac = u & 0x7fffffu;
+  const uint32_t top = i8 ? 0x7e0000u : 0x600000u;  // 127/64 - 1 and 1.75 - 1 in 23 bits
+  e -= i8 ? 6 : 8;
+  if (frac > top) e += 1;
+  if (e < -126) e = -126;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+}  // namespace svsa

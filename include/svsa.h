@@ -26,6 +26,12 @@
  *      block centroid).
  *   4. svsa_inverse_reorder -- put the output back in raster order.
  *
+ * Around them, for models that produce their tokens in pieces: the per-head
+ * norm and position rotation of queries and keys (svsa_qk_norm_rope, with its
+ * gradients), a cache of keys and values in 8-bit 64-token blocks
+ * (svsa_cache_append), the choice of blocks for each query
+ * (svsa_cache_select) and attention over the cache (svsa_cache_attn).
+ *
  * svsa_layer_create / svsa_layer_forward_host run the four steps on host
  * buffers (a layer object that owns its device memory and streams the rows
  * through the entry points above).
@@ -69,11 +75,17 @@ typedef enum {
   SVSA_ERR_TIMEOUT = 5,       /* a bounded device-side wait gave up (svsa_sync_status) */
   SVSA_ERR_RANGE = 6,         /* an input left the range the fp16 paths hold: a value
                                  given to svsa_reorder_values, or a block / sub-block mean
-                                 of the scores, beyond +-65504 or not finite; the result
-                                 saturated (svsa_sync_status) */
-  SVSA_ERR_MASK = 7           /* svsa_attn_fwd with mask.check set found a malformed list:
+                                 of the scores, beyond +-65504 or not finite, or a value
+                                 that is not finite given to an 8-bit conversion of the
+                                 block cache; the result saturated (svsa_sync_status) */
+  SVSA_ERR_MASK = 7,          /* svsa_attn_fwd with mask.check set found a malformed list:
                                  kv_cnt outside [0, cap], an index outside [0, nb) or a
                                  row not strictly ascending (svsa_sync_status) */
+  SVSA_ERR_INDEX = 8          /* a position, token map entry, page, length or list entry
+                                 that a streaming entry point read from device memory lay
+                                 outside its range; it was clamped or left out, so nothing
+                                 outside the caller's buffers was touched
+                                 (svsa_sync_status) */
 } svsa_status;
 
 typedef enum { SVSA_ORDER_RASTER = 0, SVSA_ORDER_HILBERT = 1 } svsa_order;
@@ -454,6 +466,161 @@ svsa_status svsa_layer_forward_host(svsa_layer* layer, const void* q, const void
 
 /* Free the layer (after the work queued on it has completed).  NULL is a no-op. */
 svsa_status svsa_layer_destroy(svsa_layer* layer);
+
+/* ---- streaming: norm and rotation, and a block cache in 8 bits ------------ */
+
+/* A model that produces its tokens in pieces (frames of a stream, single
+ * tokens) calls, per layer and piece: svsa_qk_norm_rope on the projection's
+ * queries and keys, svsa_cache_append with the new keys and values, and
+ * svsa_cache_attn, over the whole cache or over the blocks that
+ * svsa_cache_select chooses for each query.  (Additions of this library: the
+ * method descriptions have no counterpart.)  None of them copies to the host
+ * or depends on host values of the lengths, so a captured graph stays valid
+ * while the cache grows within its table. */
+
+typedef enum { SVSA_BF16 = 0, SVSA_F16 = 1 } svsa_dtype;
+
+/* Which two values of a row turn together. */
+typedef enum {
+  SVSA_PAIR_ADJACENT = 0,     /* (2i, 2i + 1) */
+  SVSA_PAIR_HALVES = 1        /* (i, i + d/2) */
+} svsa_pairing;
+
+typedef struct {
+  int32_t B, heads_q, heads_k;  /* heads_k = 0: no keys (k, wk, yk and their gradients unused) */
+  int32_t N, rows;              /* tokens, and rows of the outputs (N without a token map) */
+  int32_t d;                    /* 64 or 128 */
+  int32_t dtype;                /* svsa_dtype of q, k and the outputs */
+  int32_t pairing;              /* svsa_pairing */
+  int32_t axes;                 /* position axes, [0, 3]; 0 = norm only */
+  int32_t pairs[3];             /* pairs of each axis, the first axis first; their sum is d/2 */
+  int32_t table_rows;           /* rows of cos and sin */
+  float eps;                    /* >= 0 */
+  int64_t pos_stride;           /* int32 elements between the batches' positions; 0 = shared */
+  int64_t q_stride[3];          /* elements between batches, heads and tokens of q ... */
+  int64_t k_stride[3];          /* ... and of k: multiples of 8; a row's d values are contiguous */
+  int64_t dq_stride[3];         /* svsa_qk_norm_rope_bwd: the same of dq and dk */
+  int64_t dk_stride[3];
+} svsa_norm_rope;
+
+/* Per-head RMS norm of q and k, position rotation and token order, in one pass:
+ *   yq[b, h, i, :] = R(pos[b, n]) (x / sqrt(mean(x^2) + eps) * wq),  x = q[b, h, n, :],  n = map[i]
+ * and yk in the same way with wk.  R turns pair i of a row, (a, b), into
+ * (a cos - b sin, a sin + b cos) with cos[p, i], sin[p, i], p the token's
+ * position on the pair's axis.  Arithmetic in fp32, one rounding at the end.
+ * q, k: strided, 16-byte aligned (views of a fused projection output will do).
+ * yq, yk: [B, heads, rows, d], contiguous, not overlapping the inputs.
+ * wq, wk: fp32 [d] or NULL (ones).  cos, sin: fp32 [table_rows, d/2] and pos:
+ * int32 [B or 1][N][axes] (NULL when axes = 0).  map: int32 [rows], -1 = a row
+ * of zeros (svsa_build_perm's perm), or NULL = row i is token i.  With a map
+ * this takes the place of svsa_reorder for q and k. */
+svsa_status svsa_qk_norm_rope(const void* q, const void* k, const float* wq, const float* wk, const float* cos,
+                              const float* sin, const int32_t* pos, const int32_t* map, void* yq, void* yk,
+                              const svsa_norm_rope* p, void* stream);
+
+/* Gradients of svsa_qk_norm_rope, from dyq, dyk [B, heads, rows, d] and the
+ * forward's inputs: dq, dk [B, heads, N, d] with strides of their own (views
+ * of one buffer will do; their rows must not overlap, and memory between them
+ * is left as it was) and dwq, dwk fp32 [d] (NULL: not wanted).  imap: int32 [N], the output row of each token
+ * (svsa_build_perm's iperm; -1 = none, a zero gradient), or NULL without a
+ * map; the forward's map must not name a token twice.  The sums over the rows
+ * run in a fixed order: the same call gives the same bits.  ws:
+ * svsa_qk_norm_rope_bwd_workspace_bytes(p) bytes of device memory. */
+size_t svsa_qk_norm_rope_bwd_workspace_bytes(const svsa_norm_rope* p);
+svsa_status svsa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* q, const void* k, const float* wq,
+                                  const float* wk, const float* cos, const float* sin, const int32_t* pos,
+                                  const int32_t* imap, void* dq, void* dk, float* dwq, float* dwk,
+                                  const svsa_norm_rope* p, void* ws, size_t ws_bytes, void* stream);
+
+typedef enum {
+  SVSA_CODE_E4M3 = 0,         /* 4 exponent and 3 fraction bits, largest value 448 */
+  SVSA_CODE_I8 = 1            /* whole numbers -127 .. 127 */
+} svsa_code;
+
+/* Keys and values of B sequences in 8 bits, in pages of one 64-token block:
+ * token n of sequence b is row n % 64 of page table[b][n / 64], and stands for
+ * code * scale, one scale per page and head.  A page may be read by several
+ * sequences, but only one sequence may append to it.  Caller-owned device
+ * memory. */
+typedef struct {
+  void* k;                    /* [n_pages, heads, 64, d] codes */
+  void* v;
+  float* k_scale;             /* [n_pages, heads], >= 0 */
+  float* v_scale;
+  int8_t* mean;               /* nullable [n_pages, heads, d]: each block's mean key in */
+  float* mean_scale;          /* whole numbers, and its scale [n_pages, heads] */
+  const int32_t* table;       /* [B, max_blocks] pages; entries past a sequence's blocks are not read */
+  const int32_t* len;         /* [B] tokens of each sequence, [0, 64 * max_blocks] */
+  int32_t B, heads, d;        /* d: 64 or 128 */
+  int32_t code;               /* svsa_code */
+  int32_t n_pages, max_blocks;
+} svsa_cache;
+
+typedef struct {
+  int32_t N;                  /* tokens per sequence in k and v */
+  int32_t dtype;              /* svsa_dtype */
+  int64_t k_stride[3];        /* elements between batches, heads and tokens: multiples of 8 */
+  int64_t v_stride[3];
+} svsa_cache_tokens;
+
+/* Append k, v (strided [B, heads, N, d]) to the cache at positions len[b], ...:
+ * n_new[b] tokens of sequence b (NULL: N of each; the rest of a padded batch
+ * is not read).  len holds the lengths before the call; len_out (nullable, not
+ * len itself) receives the lengths after it.  For each block that receives
+ * tokens, and for keys and values apart,
+ *   scale = max(the block's scale, if it held tokens; the smallest power of
+ *           two s with max |new values| / s <= 448 (e4m3) or 127 (int8))
+ *   code  = round to nearest even(value / scale),
+ * and where the scale grew, the codes that were there are rounded again from
+ * the values they stood for.  Rows past the last token stay as they were.
+ * With mean: mean key of the block's codes, sum / count in fp32, rounded to
+ * whole numbers under the smallest power of two that holds it in 127; the sum
+ * is exact, so the result depends on the codes alone.  A value that is not
+ * finite saturates (NaN becomes 0) and is reported as SVSA_ERR_RANGE. */
+svsa_status svsa_cache_append(const svsa_cache* c, const void* k, const void* v, const int32_t* n_new,
+                              int32_t* len_out, const svsa_cache_tokens* p, void* stream);
+
+/* Queries over the cache: q [B, heads_q, Tq, d], contiguous; query head h
+ * reads key head h / (heads_q / heads).  causal = 1: the queries are the last
+ * Tq tokens of their sequences, and query t sees the keys 0 .. len - Tq + t;
+ * causal = 0: each sees all len keys. */
+typedef struct {
+  int32_t heads_q, Tq;        /* heads_q a multiple of the cache's heads */
+  int32_t dtype;              /* svsa_dtype of q and o */
+  int32_t causal;
+  int32_t cap;                /* entries of a query's list */
+  int32_t first, last;        /* svsa_cache_select: blocks kept at the start and at the end */
+} svsa_cache_query;
+
+/* Choose key blocks for every query and key head: of the blocks that the query
+ * sees, the first `first`, the last `last` and then those with the largest
+ *   score = max over the head's group of  q8 . mean8 * (q's scale * mean_scale),
+ * q8 = q in whole numbers under its row's smallest power of two that holds it
+ * in 127; up to cap in all, equal scores by the lower index.  Dot products of
+ * whole numbers are exact, so the lists depend on nothing but the inputs.
+ * idx [B, Tq, heads, cap]: ascending, then zeros; cnt [B, Tq, heads].
+ * first + last <= cap; max_blocks <= 65536; heads_q / heads <= 128; mean and
+ * mean_scale required.  A value of q that is not finite saturates (NaN counts
+ * 0) and is reported as SVSA_ERR_RANGE. */
+svsa_status svsa_cache_select(const svsa_cache* c, const void* q, int32_t* idx, int32_t* cnt,
+                              const svsa_cache_query* p, void* stream);
+
+/* Attention of the queries over the cache:
+ *   o[b, h, t, :] = sum_n softmax_n(q . k_n / sqrt(d)) v_n
+ * over the keys that the query sees, or (idx, cnt given, as svsa_cache_select
+ * writes them) over those of them in the query's listed blocks.  A list is
+ * strictly ascending; an entry that is not, or that lies past the sequence, is
+ * left out and reported (SVSA_ERR_INDEX).  A query that sees no key gives
+ * zeros and lse = -inf; a query row with a value that is not finite gives NaN.
+ * Rows of the pages past len may hold anything.  o like q; lse nullable fp32
+ * [B, heads_q, Tq], natural log.  Softmax weights are rounded to fp16 (as in
+ * svsa_attn_fwd), statistics and sums are fp32; the result does not depend on
+ * the state of the GPU: the same call gives the same bits.  ws:
+ * svsa_cache_attn_workspace_bytes(c, p) bytes of device memory, for one call
+ * at a time. */
+size_t svsa_cache_attn_workspace_bytes(const svsa_cache* c, const svsa_cache_query* p);
+svsa_status svsa_cache_attn(const svsa_cache* c, const void* q, const int32_t* idx, const int32_t* cnt, void* o,
+                            float* lse, const svsa_cache_query* p, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- status ------------------------------------------------------------- */
 

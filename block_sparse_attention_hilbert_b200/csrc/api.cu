@@ -102,7 +102,8 @@ cudaError_t cache_flags(unsigned int* v, cudaStream_t st);
 size_t cache_attn_workspace_bytes(int d);
 cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal,
                               const int32_t* idx, const int32_t* cnt, int cap, void* o, float* lse, void* ws,
-                              cudaStream_t st);
+                              int* launches, cudaStream_t st);
+long long cache_attn_units(const CacheArgs& c, int heads_q, int Tq, const int32_t* idx, int cap);
 cudaError_t cattn_flags(unsigned int* v, cudaStream_t st);
 cudaError_t cattn_error(unsigned int* code, cudaStream_t st);
 svsa_status record_error(svsa_status st, const char* msg);
@@ -1159,12 +1160,15 @@ svsa_status svsa_cache_attn(const svsa_cache* c, const void* q, const int32_t* i
     SVSA_PTR(cnt, "cnt");
     if (p->cap < 1 || p->cap > (1 << 24)) return fail(SVSA_ERR_INVALID_ARG, "cap=%d must be in [1, 2^24]", p->cap);
   }
+  const long long units = cache_attn_units(a, p->heads_q, p->Tq, idx, p->cap);
+  if (units >= (1LL << 31)) return fail(SVSA_ERR_UNSUPPORTED, "%lld block visits exceed 2^31", units);
   const size_t need = cache_attn_workspace_bytes(c->d);
   SVSA_PTR(ws, "ws");
   if (ws_bytes < need) return fail(SVSA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
-  return cuda_status(counted(launch_cache_attn(a, q, p->heads_q, p->Tq, p->dtype == SVSA_F16, p->causal, idx, cnt,
-                                               p->cap, o, lse, ws, (cudaStream_t)stream), 2),
-                     "cache_attn launch");
+  int launches = 0;
+  const cudaError_t e = launch_cache_attn(a, q, p->heads_q, p->Tq, p->dtype == SVSA_F16, p->causal, idx, cnt, p->cap,
+                                          o, lse, ws, &launches, (cudaStream_t)stream);
+  return cuda_status(counted(e, launches), "cache_attn launch");
 }
 
 svsa_status svsa_sync_status(void* stream) {

@@ -45,8 +45,6 @@ static __device__ unsigned int g_cattn_flags;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr float kShift = 14.f;              // weights are held times 2^kShift
 constexpr int kMinUnits = 8;                // blocks of a CTA at least, where there are as many
 
@@ -287,16 +285,17 @@ struct Window {
   float ks, vs;
 };
 
+template <int WARPS>
 __device__ __forceinline__ Window load_window(const AttnArgs& p, const Segment& s, int first, int len) {
   Window w;
   const int lane = threadIdx.x % 32;
   const int left = s.j1 - first;
-  w.n = left > 0 ? min(32, (left + kWarps - 1) / kWarps) : 0;
+  w.n = left > 0 ? min(32, (left + WARPS - 1) / WARPS) : 0;
   w.row = 0;
   w.tok = 1 << 30;
   w.ks = w.vs = 0.f;
   if (lane < w.n) {
-    int j = first + lane * kWarps;
+    int j = first + lane * WARPS;
     bool ok = p.idx || len > 0;              // an empty sequence has one unit, and nothing in it
     if (p.idx) {
       const int32_t* list = p.idx + (((long long)s.b * p.Tq + s.t) * p.c.heads + s.h) * p.cap;
@@ -319,15 +318,18 @@ __device__ __forceinline__ Window load_window(const AttnArgs& p, const Segment& 
   return w;
 }
 
-// Shared memory: the warps' rings, and the area where they join their sums.
+// Shape of a CTA.  A warp's ring holds its tiles in flight; when a segment is
+// done it holds the warp's sums, to be joined.
 template <int D, int NR>
-struct Smem {
+struct Cta {
+  static constexpr int kWarps = NR == 1 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kTile = kBlock * D;
-  static constexpr int kRing = NR == 1 ? 3 : 2;                      // tiles in flight per warp
+  static constexpr int kRing = (NR == 1 ? 2 : 3) * (128 / D);        // tiles in flight per warp
   static constexpr int kRows = 8 * NR;
-  static constexpr int kPitch = D + 4;                               // floats of a row in the joining area
-  static constexpr int kRingBytes = kWarps * kRing * kTile;
-  static constexpr int kTotal = kRingBytes + kWarps * kRows * kPitch * 4 + 1024;   // + alignment of the tiles
+  static constexpr int kPitch = D + 4;                               // floats of a row of sums
+  static constexpr int kSmem = kWarps * kRing * kTile + 1024;        // + alignment of the tiles
+  static_assert(kRows * kPitch * 4 <= kRing * kTile, "the sums fit the ring");
 };
 
 // A finished row's four columns from col on, or the CTA's share of them.
@@ -346,11 +348,11 @@ __device__ __forceinline__ void write_out(const AttnArgs& p, const Segment& s, i
 }
 
 template <int D, typename T, bool I8, int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cta<D, NR>::kThreads, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   const __grid_constant__ AttnArgs p) {
-  using S = Smem<D, NR>;
-  constexpr int ROWS = S::kRows, RING = S::kRing, TILE = S::kTile;
+  using S = Cta<D, NR>;
+  constexpr int ROWS = S::kRows, RING = S::kRing, TILE = S::kTile, kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int MT = D / 16;                 // output tiles of 16 columns; also the k steps of K Q^T
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t bars[kWarps * RING];
@@ -359,7 +361,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
   const uint32_t ring0 = (tc::su32(dyn) + 1023u) & ~1023u;
-  float* merge = reinterpret_cast<float*>(dyn + (ring0 - tc::su32(dyn)) + S::kRingBytes);
+  float* const sums = reinterpret_cast<float*>(dyn + (ring0 - tc::su32(dyn)));
+  constexpr int SUMS = RING * TILE / 4;      // floats between two warps' rings
   const uint32_t ring = ring0 + warp * (RING * TILE);
   const uint32_t bar = tc::su32(bars) + warp * (RING * 8);
   const Shares sh = shares_of(p);
@@ -415,11 +418,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
     // windows of blocks: `cur` is consumed while loads may run into `nxt`
     int at = s.j0 + warp;
-    Window cur = load_window(p, s, at, len);
+    Window cur = load_window<kWarps>(p, s, at, len);
     at += 32 * kWarps;
     Window nxt;
     nxt.n = 0;
-    if (at < s.j1) nxt = load_window(p, s, at, len);
+    if (at < s.j1) nxt = load_window<kWarps>(p, s, at, len);
     at += 32 * kWarps;
     uint32_t fetched = 0;                     // tiles of `cur` (and on into `nxt`) asked for: K then V of each block
     auto fetch = [&]() {                      // one more tile, if there is one
@@ -627,11 +630,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       fetched -= 2u * (uint32_t)cur.n;
       cur = nxt;
       nxt.n = 0;
-      if (at < s.j1) nxt = load_window(p, s, at, len);
+      if (at < s.j1) nxt = load_window<kWarps>(p, s, at, len);
       at += 32 * kWarps;
     }
 
     // join the warps: maxima and row sums, then each warp's sums under the common maximum
+    // (every tile that this warp asked for has been read, so its ring is free)
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -652,7 +656,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       for (int e = 0; e < 2; ++e) {
         const int row = 8 * r + 2 * c + e;
         if (row < rows) {
-          float* to = merge + (warp * ROWS + row) * S::kPitch + g * (D / 8);
+          float* to = sums + warp * SUMS + row * S::kPitch + g * (D / 8);
 #pragma unroll
           for (int n = 0; n < MT; n += 2)
             *reinterpret_cast<float4*>(to + 2 * n) = make_float4(o[n][r][e], o[n][r][e + 2], o[n + 1][r][e], o[n + 1][r][e + 2]);
@@ -669,7 +673,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = tc::ex2(stat_m[w][row] - z);
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * ROWS + row) * S::kPitch + col);
+        const float4 v = *reinterpret_cast<const float4*>(sums + w * SUMS + row * S::kPitch + col);
         sum += stat_l[w][row] * f;
         acc.x += v.x * f;
         acc.y += v.y * f;
@@ -690,7 +694,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
       }
     }
-    __syncthreads();                           // the statistics and the joining area are free again
+    tc::fence_async_smem();                    // the next tiles arrive through the async proxy
+    __syncthreads();                           // the statistics and the rings are free again
   }
 }
 
@@ -774,10 +779,10 @@ bool map_codes(CUtensorMap* m, const void* base, long long rows, int d) {
 template <int D, typename T, bool I8, int NR>
 cudaError_t run(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& p, cudaStream_t st) {
   auto kernel = cache_attn_kernel<D, T, I8, NR>;
-  constexpr int smem = Smem<D, NR>::kTotal;
+  constexpr int smem = Cta<D, NR>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<p.grid, kThreads, smem, st>>>(mk, mv, p);
+  kernel<<<p.grid, Cta<D, NR>::kThreads, smem, st>>>(mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
   cudaLaunchConfig_t cfg{};
@@ -821,7 +826,7 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   // kernel takes 3 us, and so does a round trip of the partial sums.
   const long long items = (long long)c.B * (idx ? Tq : 1) * c.heads * p.tiles;
   const long long rounds = (items + kNumSMs - 1) / kNumSMs;
-  p.whole = (idx ? cap : c.max_blocks) <= 2 * kWarps || (idx && items * 20 >= rounds * kNumSMs * 19);
+  p.whole = (idx ? cap : c.max_blocks) <= 16 || (idx && items * 20 >= rounds * kNumSMs * 19);
   CUtensorMap mk, mv;
   const long long map_rows = (long long)c.n_pages * c.heads * kBlock;
   if (!map_codes(&mk, c.k, map_rows, c.d) || !map_codes(&mv, c.v, map_rows, c.d)) return cudaErrorInvalidValue;

@@ -218,6 +218,33 @@ __device__ __forceinline__ void mma_first(float d[4], const uint32_t a[4], uint3
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// Two fp32 lanes in one instruction (sm_100), each rounded as its scalar form.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split2(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 // An 8 x 8 matrix of 16-bit values (row g of lane 4 g + c: columns 2 c, 2 c + 1), transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -475,19 +502,15 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     }
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
-    float o[MT][NR][4];                       // O^T: columns g (+ 8) of tile mt, rows 2 c, 2 c + 1
-    float m[NR][2], l[NR][2];
+    F2 o[MT][NR][2];                          // O^T: column g (+ 8) of tile mt, rows 2 c and 2 c + 1
+    float m[NR][2];
+    F2 l[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
+      m[r][0] = m[r][1] = -INFINITY;
+      l[r] = f2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[r][e] = -INFINITY;
-        l[r][e] = 0.f;
-      }
-#pragma unroll
-      for (int n = 0; n < MT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][r][e] = 0.f;
+      for (int n = 0; n < MT; ++n) o[n][r][0] = o[n][r][1] = f2(0.f, 0.f);
     }
 
     while (cur.n > 0) {
@@ -529,49 +552,52 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         __syncwarp();
         fetch();                              // into the K tile's place
 
-        // online softmax of the rows 2 c and 2 c + 1 (log2 units)
+        // online softmax of the rows 2 c and 2 c + 1 (log2 units): the scale joins
+        // in the exponent, p = 2^(s f - m + 14)
+        if (tok + kBlock > lim_min) {         // warp-uniform
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int mt = 0; mt < 4; ++mt)
+                if (tok + 16 * mt + g + 8 * (e >> 1) >= lim[r][e & 1]) sc[mt][r][e] = -INFINITY;
+        }
         uint32_t pf[4][NR][2];
-        float al[NR][2];
+        F2 al[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          float z[2];
+          float z[2], f[2], a[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = fac[r][e] * ks;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-              sc[mt][r][e] *= f;
-              sc[mt][r][e + 2] *= f;
-            }
-            if (tok + kBlock > lim_min) {     // warp-uniform
-#pragma unroll
-              for (int mt = 0; mt < 4; ++mt) {
-                if (tok + 16 * mt + g >= lim[r][e]) sc[mt][r][e] = -INFINITY;
-                if (tok + 16 * mt + g + 8 >= lim[r][e]) sc[mt][r][e + 2] = -INFINITY;
-              }
-            }
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) mx = tc::max3(mx, sc[mt][r][e], sc[mt][r][e + 2]);
+            f[e] = fac[r][e] * ks;
+            if (f[e] == 0.f) f[e] = 1.17549435e-38f;      // keeps -inf apart from 0 * -inf
+            float mx = tc::max3(sc[0][r][e], sc[0][r][e + 2], sc[1][r][e]);
+            mx = tc::max3(mx, sc[1][r][e + 2], sc[2][r][e]);
+            mx = tc::max3(mx, sc[2][r][e + 2], sc[3][r][e]);
+            mx = fmaxf(mx, sc[3][r][e + 2]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float n = fmaxf(m[r][e], mx);
+            const float n = fmaxf(m[r][e], mx * f[e]);
             z[e] = n == -INFINITY ? 0.f : n;
-            al[r][e] = tc::ex2(m[r][e] - z[e]);
+            a[e] = tc::ex2(m[r][e] - z[e]);
             m[r][e] = n;
-            z[e] -= kShift;
-            l[r][e] *= al[r][e];
           }
+          al[r] = f2(a[0], a[1]);
+          const F2 ff = f2(f[0], f[1]), zz = f2(kShift - z[0], kShift - z[1]);
+          l[r] = mul2(l[r], al[r]);
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
-            const float e0 = tc::ex2(sc[mt][r][0] - z[0]), e1 = tc::ex2(sc[mt][r][1] - z[1]);
-            const float e2 = tc::ex2(sc[mt][r][2] - z[0]), e3 = tc::ex2(sc[mt][r][3] - z[1]);
-            l[r][0] += e0 + e2;
-            l[r][1] += e1 + e3;
-            pf[mt][r][0] = transpose8(tc::pack_f16x2(e0, e1));
-            pf[mt][r][1] = transpose8(tc::pack_f16x2(e2, e3));
-          }
+          for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int h8 = 0; h8 < 2; ++h8) {
+              float e0, e1;
+              split2(fma2(f2(sc[mt][r][2 * h8], sc[mt][r][2 * h8 + 1]), ff, zz), e0, e1);
+              e0 = tc::ex2(e0);
+              e1 = tc::ex2(e1);
+              l[r] = add2(l[r], f2(e0, e1));
+              pf[mt][r][h8] = transpose8(tc::pack_f16x2(e0, e1));
+            }
         }
 
         // O^T += vs V^T P^T on the codes: rows g and g + 8 of tile mt are
@@ -579,7 +605,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         // codes of its four tokens per step
         float pv[MT][NR][4];
         const uint32_t vt = arrived();
-        const bool edge = tok + kBlock > len;  // rows past the sequence hold anything: zero weights times NaN
+        if (tok + kBlock > len) {              // rows past the sequence hold anything (zero weights times NaN): clear them
+          for (int x = max(len - tok, 0) * (D / 16) + lane; x < kBlock * (D / 16); x += 32)
+            tc::st_shared_v4(vt + 16 * x, 0u, 0u, 0u, 0u);      // (the swizzle keeps a 16-byte piece in its row)
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t w[4][D / 32];              // tokens 16 k + 2 c, + 1, + 8, + 9
@@ -592,10 +622,6 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             } else {
               const uint2 a = lds64(vt + k * 1024 + row * 64 + (((g >> 1) ^ c) << 4) + (g & 1) * 8);
               w[r][0] = a.x; w[r][1] = a.y;
-            }
-            if (edge && tok + 16 * k + row >= len) {
-#pragma unroll
-              for (int i2 = 0; i2 < D / 32; ++i2) w[r][i2] = 0u;
             }
           }
 #pragma unroll
@@ -618,14 +644,17 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
           }
         }
+        if (tok + kBlock > len) tc::fence_async_smem();        // (the clearing above, before the next tile arrives)
         __syncwarp();
         fetch();                              // into the V tile's place
+        const F2 vv = f2(vs, vs);
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
           for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][r][e] = o[n][r][e] * al[r][e & 1] + pv[n][r][e] * vs;
+            for (int h8 = 0; h8 < 2; ++h8)
+              o[n][r][h8] = fma2(f2(pv[n][r][2 * h8], pv[n][r][2 * h8 + 1]), vv, mul2(o[n][r][h8], al[r]));
       }
       fetched -= 2u * (uint32_t)cur.n;
       cur = nxt;
@@ -636,32 +665,33 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
     // join the warps: maxima and row sums, then each warp's sums under the common maximum
     // (every tile that this warp asked for has been read, so its ring is free)
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = l[r][e];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (g == 0) {
-          stat_m[warp][8 * r + 2 * c + e] = m[r][e];
-          stat_l[warp][8 * r + 2 * c + e] = v;
-        }
-      }
     const int rows = min(ROWS, (s.t >= 0 ? p.group : p.group * p.Tq) - s.tile * ROWS);
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
+    for (int r = 0; r < NR; ++r) {
+      float v[2];
+      split2(l[r], v[0], v[1]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        v[e] += __shfl_xor_sync(0xffffffffu, v[e], 4);
+        v[e] += __shfl_xor_sync(0xffffffffu, v[e], 8);
+        v[e] += __shfl_xor_sync(0xffffffffu, v[e], 16);
         const int row = 8 * r + 2 * c + e;
+        if (g == 0) {
+          stat_m[warp][row] = m[r][e];
+          stat_l[warp][row] = v[e];
+        }
         if (row < rows) {
           float* to = sums + warp * SUMS + row * S::kPitch + g * (D / 8);
 #pragma unroll
-          for (int n = 0; n < MT; n += 2)
-            *reinterpret_cast<float4*>(to + 2 * n) = make_float4(o[n][r][e], o[n][r][e + 2], o[n + 1][r][e], o[n + 1][r][e + 2]);
+          for (int n = 0; n < MT; n += 2) {
+            float x[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split2(o[n + i / 2][r][i % 2], x[i][0], x[i][1]);
+            *reinterpret_cast<float4*>(to + 2 * n) = make_float4(x[0][e], x[1][e], x[2][e], x[3][e]);
+          }
         }
       }
+    }
     __syncthreads();
     for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
       const int row = x / (D / 4), col = x % (D / 4) * 4;

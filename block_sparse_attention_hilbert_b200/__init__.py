@@ -10,6 +10,7 @@ call raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -372,46 +373,28 @@ def svsa_inverse_reorder(op, o, iperm, s: Shape, stream=None) -> None:
 
 # ---- streaming: norm and rotation, block cache --------------------------------
 #
-# The structures below are made from tensors, which are checked for what the C
-# entry points cannot see (types, shapes, devices, strides).  A call runs on the
-# current stream of its tensors' device, whichever device is current.
+# Tensor checks (types, shapes, strides, devices) and marshalling of these are
+# in the native module (csrc/binding.cpp): a misfit raises ValueError.  A call
+# runs on `stream`, or the current stream of its tensors' device, whichever
+# device is current.
 
-_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-_CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_I8}
-
-
-def _bad(t, dtype, shape, device: int, what: str):
-    raise ValueError(f"{what}: expected a contiguous {dtype} tensor {tuple(shape)} on device {device}, got "
-                     f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+_native_module = None
 
 
-def _of(t, dtype, shape, device: int, what: str):
-    """The address of t, which must be contiguous and of this type, shape and device (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        _bad(t, dtype, shape, device, what)
-    return t.data_ptr()
-
-
-def _view(t, dtype, shape, stride, device: int, what: str) -> int:
-    """The address of a view with these strides and a contiguous last dimension."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or t.stride() != (*stride, 1):
-        raise ValueError(f"{what}: expected {dtype} {tuple(shape)} with strides {(*stride, 1)} on device {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
-
-def _call(fn: str, device: int, stream, *args) -> None:
-    """The entry point `fn` on `stream`, or the current stream of `device`."""
-    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if device == torch.cuda.current_device():
-        status = getattr(_lib or lib(), fn)(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            status = getattr(_lib or lib(), fn)(*args, handle)
-    if status != 0:
-        _check(status, fn)
+def _native():
+    """The native module of the streaming calls (raises if it has not been built)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        path = os.path.join(_PKG, "lib", "_svsa_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m block_sparse_attention_hilbert_b200.build`")
+        spec = importlib.util.spec_from_file_location("_svsa_binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.init(NormRope, Cache, CacheTokens, CacheQuery)
+        _native_module = m
+    return _native_module
 
 
 def norm_rope_params(q, k, cos=None, pos=None, *, rows: int | None = None, pairs=(), halves: bool = False,
@@ -419,139 +402,68 @@ def norm_rope_params(q, k, cos=None, pos=None, *, rows: int | None = None, pairs
     """Parameters of svsa_qk_norm_rope for q [B, heads_q, N, d] and k [B, heads_k, N, d] or None (views with a
     contiguous last dimension).  pairs: pairs of each position axis; pos int32 [B or 1, N, axes]; cos fp32
     [table_rows, d / 2].  rows: rows of the outputs (N without a token map)."""
-    B, hq, N, d = q.shape
-    sq = q.stride()
-    if q.dtype not in _DTYPES or sq[3] != 1:
-        raise ValueError(f"q: {q.dtype} strides {sq} (supported: bfloat16 and float16, a contiguous last dimension)")
-    hk, sk = 0, (0, 0, 0)
-    if k is not None:
-        hk, sk = k.shape[1], k.stride()
-        if k.dtype is not q.dtype or k.shape != (B, hk, N, d) or sk[3] != 1:
-            raise ValueError("k: expected q's type, batch, tokens and head dim, with a contiguous last dimension")
-    axes, pos_stride, table = len(pairs), 0, 0
-    if axes:
-        if axes > 3 or pos is None or cos is None:
-            raise ValueError("to rotate, give cos, sin, pos and the pairs of at most 3 axes")
-        if pos.shape[0] == B and B > 1:
-            pos_stride = N * axes
-        table = cos.shape[0]
-    return NormRope(B, hq, hk, N, N if rows is None else rows, d, _DTYPES[q.dtype], 1 if halves else 0, axes,
-                    (*pairs,), table, eps, pos_stride, sq[:3], sk[:3], (0, 0, 0), (0, 0, 0))
-
-
-def _norm_rope_inputs(p: NormRope, q, k, wq, wk, cos, sin, pos, perm, n_perm: int, dev: int):
-    """Addresses of the inputs of the forward and the backward, checked against the parameters."""
-    B, N, d = p.B, p.N, p.d
-    dt = q.dtype
-    if _DTYPES.get(dt) != p.dtype or (k is None) != (p.heads_k == 0):
-        raise ValueError("q or k does not fit the parameters")
-    f32 = torch.float32
-    turn = (None, None, None)
-    if p.axes:
-        if cos is None or sin is None or pos is None:
-            raise ValueError("cos, sin and pos are needed to rotate")
-        turn = (_of(cos, f32, (p.table_rows, d // 2), dev, "cos"), _of(sin, f32, (p.table_rows, d // 2), dev, "sin"),
-                _of(pos, torch.int32, (B if p.pos_stride else 1, N, p.axes), dev, "pos"))
-    return (_view(q, dt, (B, p.heads_q, N, d), p.q_stride, dev, "q"),
-            None if k is None else _view(k, dt, (B, p.heads_k, N, d), p.k_stride, dev, "k"),
-            _of(wq, f32, (d,), dev, "wq"), _of(wk, f32, (d,), dev, "wk"), *turn,
-            _of(perm, torch.int32, (n_perm,), dev, "token map"))
+    return (_native_module or _native()).norm_rope_params(q, k, cos, pos, rows, pairs, halves, eps)
 
 
 def svsa_qk_norm_rope(q, k, wq, wk, cos, sin, pos, perm, yq, yk, p: NormRope, stream=None) -> None:
     """Norm, rotation and token order of q and k (k, wk, yk None without keys; perm None for raster order)."""
-    dev = q.get_device()
-    ins = _norm_rope_inputs(p, q, k, wq, wk, cos, sin, pos, perm, p.rows, dev)
-    _call("svsa_qk_norm_rope", dev, stream, *ins, _of(yq, q.dtype, (p.B, p.heads_q, p.rows, p.d), dev, "yq"),
-          _of(yk, q.dtype, (p.B, p.heads_k, p.rows, p.d), dev, "yk"), p)
+    status = (_native_module or _native()).qk_norm_rope(q, k, wq, wk, cos, sin, pos, perm, yq, yk, p, stream)
+    if status:
+        _check(status, "svsa_qk_norm_rope")
 
 
 def svsa_qk_norm_rope_bwd_workspace_bytes(p: NormRope) -> int:
-    return lib().svsa_qk_norm_rope_bwd_workspace_bytes(p)
+    return (_native_module or _native()).qk_norm_rope_bwd_workspace_bytes(p)
 
 
 def svsa_qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, cos, sin, pos, iperm, dq, dk, dwq, dwk, p: NormRope, ws,
                           ws_bytes: int, stream=None) -> None:
     """Gradients of svsa_qk_norm_rope: dq, dk in q's and k's shapes, with strides of their own; dwq, dwk fp32 [d] (or
     None).  iperm: the output row of each token (None for raster order)."""
-    dev, dt = q.get_device(), q.dtype
-    ins = _norm_rope_inputs(p, q, k, wq, wk, cos, sin, pos, iperm, p.N, dev)
-    p = NormRope.from_buffer_copy(p)
-    p.dq_stride = dq.stride()[:3]
-    if k is not None:
-        p.dk_stride = dk.stride()[:3]
-    _call("svsa_qk_norm_rope_bwd", dev, stream, _of(dyq, dt, (p.B, p.heads_q, p.rows, p.d), dev, "dyq"),
-          _of(dyk, dt, (p.B, p.heads_k, p.rows, p.d), dev, "dyk"), *ins,
-          _view(dq, dt, (p.B, p.heads_q, p.N, p.d), p.dq_stride, dev, "dq"),
-          None if k is None else _view(dk, dt, (p.B, p.heads_k, p.N, p.d), p.dk_stride, dev, "dk"),
-          _of(dwq, torch.float32, (p.d,), dev, "dwq"), _of(dwk, torch.float32, (p.d,), dev, "dwk"), p, _p(ws), ws_bytes)
+    status = (_native_module or _native()).qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, cos, sin, pos, iperm, dq, dk, dwq,
+                                                            dwk, p, ws, ws_bytes, stream)
+    if status:
+        _check(status, "svsa_qk_norm_rope_bwd")
 
 
 def block_cache(k, v, k_scale, v_scale, table, length, mean=None, mean_scale=None) -> Cache:
     """The cache structure over these tensors (keep them alive while it is used): k, v codes [n_pages, heads, 64, d]
     (torch.float8_e4m3fn or torch.int8), scales fp32 [n_pages, heads], table int32 [B, max_blocks], length int32
     [B], and for block selection mean int8 [n_pages, heads, d] with mean_scale fp32 [n_pages, heads]."""
-    dev, dt, shape = k.get_device(), k.dtype, k.shape
-    if dt not in _CODES or len(shape) != 4 or shape[2] != BLOCK:
-        raise ValueError(f"k: {dt} {tuple(shape)} (supported: float8_e4m3fn or int8 codes [n_pages, heads, {BLOCK}, d])")
-    n, h, _, d = shape
-    B, width = table.shape
-    f32, i32 = torch.float32, torch.int32
-    c = Cache(_of(k, dt, shape, dev, "k"), _of(v, dt, shape, dev, "v"), _of(k_scale, f32, (n, h), dev, "k_scale"),
-              _of(v_scale, f32, (n, h), dev, "v_scale"), _of(mean, torch.int8, (n, h, d), dev, "mean"),
-              _of(mean_scale, f32, (n, h), dev, "mean_scale"), _of(table, i32, (B, width), dev, "table"),
-              _of(length, i32, (B,), dev, "length"), B, h, d, _CODES[dt], n, width)
-    c.device = dev
-    return c
+    return (_native_module or _native()).block_cache(k, v, k_scale, v_scale, table, length, mean, mean_scale)
 
 
 def cache_tokens(k, v) -> CacheTokens:
     """Parameters of svsa_cache_append for k, v [B, heads, N, d] (views with a contiguous last dimension)."""
-    sk, sv = k.stride(), v.stride()
-    if k.dtype not in _DTYPES or len(sk) != 4 or v.dtype is not k.dtype or v.shape != k.shape or sk[3] != 1 or sv[3] != 1:
-        raise ValueError("k and v: expected bfloat16 or float16 [B, heads, N, d] of one type and shape, with a "
-                         "contiguous last dimension")
-    return CacheTokens(k.shape[2], _DTYPES[k.dtype], sk[:3], sv[:3])
+    return (_native_module or _native()).cache_tokens(k, v)
 
 
 def svsa_cache_append(c: Cache, k, v, n_new, len_out, p: CacheTokens, stream=None) -> None:
-    dev, shape = c.device, (c.B, c.heads, p.N, c.d)
-    if _DTYPES.get(k.dtype) != p.dtype:
-        raise ValueError("k does not fit the parameters")
-    _call("svsa_cache_append", dev, stream, c, _view(k, k.dtype, shape, p.k_stride, dev, "k"),
-          _view(v, k.dtype, shape, p.v_stride, dev, "v"), _of(n_new, torch.int32, (c.B,), dev, "n_new"),
-          _of(len_out, torch.int32, (c.B,), dev, "len_out"), p)
+    status = (_native_module or _native()).cache_append(c, k, v, n_new, len_out, p, stream)
+    if status:
+        _check(status, "svsa_cache_append")
 
 
 def cache_query(q, *, causal: bool = True, cap: int = 0, first: int = 0, last: int = 0) -> CacheQuery:
     """Parameters of svsa_cache_select and svsa_cache_attn for q [B, heads_q, Tq, d]."""
-    shape = q.shape
-    if q.dtype not in _DTYPES or len(shape) != 4:
-        raise ValueError(f"q: {q.dtype} {tuple(shape)} (supported: bfloat16 and float16 [B, heads, Tq, d])")
-    return CacheQuery(shape[1], shape[2], _DTYPES[q.dtype], 1 if causal else 0, cap, first, last)
-
-
-def _cache_query_inputs(c: Cache, q, idx, cnt, p: CacheQuery):
-    if _DTYPES.get(q.dtype) != p.dtype:
-        raise ValueError("q does not fit the parameters")
-    B, Tq, h, dev = c.B, p.Tq, c.heads, c.device
-    return (_of(q, q.dtype, (B, p.heads_q, Tq, c.d), dev, "q"), _of(idx, torch.int32, (B, Tq, h, p.cap), dev, "idx"),
-            _of(cnt, torch.int32, (B, Tq, h), dev, "cnt"))
+    return (_native_module or _native()).cache_query(q, causal, cap, first, last)
 
 
 def svsa_cache_select(c: Cache, q, idx, cnt, p: CacheQuery, stream=None) -> None:
-    _call("svsa_cache_select", c.device, stream, c, *_cache_query_inputs(c, q, idx, cnt, p), p)
+    status = (_native_module or _native()).cache_select(c, q, idx, cnt, p, stream)
+    if status:
+        _check(status, "svsa_cache_select")
 
 
 def svsa_cache_attn_workspace_bytes(c: Cache, p: CacheQuery) -> int:
-    return lib().svsa_cache_attn_workspace_bytes(c, p)
+    return (_native_module or _native()).cache_attn_workspace_bytes(c, p)
 
 
 def svsa_cache_attn(c: Cache, q, idx, cnt, o, lse, p: CacheQuery, ws, ws_bytes: int, stream=None) -> None:
     """Attention over the cache; with idx and cnt (both or neither) over each query's listed blocks."""
-    ins = _cache_query_inputs(c, q, idx, cnt, p)
-    _call("svsa_cache_attn", c.device, stream, c, *ins, _of(o, q.dtype, q.shape, c.device, "o"),
-          _of(lse, torch.float32, q.shape[:3], c.device, "lse"), p, _p(ws), ws_bytes)
+    status = (_native_module or _native()).cache_attn(c, q, idx, cnt, o, lse, p, ws, ws_bytes, stream)
+    if status:
+        _check(status, "svsa_cache_attn")
 
 
 def svsa_launch_count() -> int:

@@ -4,7 +4,10 @@
 
 Each csrc/*.cu compiles to an object under <repo>/_build/ (in parallel, and
 only when its sources are newer than the object), then everything links into
-block_sparse_attention_hilbert_b200/lib/libsvsa.so.
+block_sparse_attention_hilbert_b200/lib/libsvsa.so.  csrc/binding.cpp (tensor
+checks and marshalling of the streaming entry points, against torch's headers)
+becomes the Python module lib/_svsa_binding.so, which links to libsvsa.so
+beside it.
 """
 from __future__ import annotations
 
@@ -23,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsvsa.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(LIBDIR, "_svsa_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -54,14 +59,49 @@ def _compile(nvcc: str, src: str, force: bool, verbose: bool) -> tuple[str, str]
     return obj, res.stderr
 
 
+def _compile_binding(force: bool) -> str:
+    """The object of the Python module; its own step, so that it runs beside the nvcc ones."""
+    import sysconfig
+
+    import torch
+    obj = os.path.join(BUILD, "binding.o")
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= _newest_dep(BINDING_SRC):
+        return obj
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-isystem", sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the compiler failed for {BINDING_SRC}:\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj: str, force: bool) -> None:
+    import torch
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(obj),
+                                                                                 os.path.getmtime(LIB)):
+        return
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", BINDING, obj, "-L", LIBDIR, "-lsvsa", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+
+
 def build(jobs: int = 0, force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
-    with ThreadPoolExecutor(jobs) as ex:
+    with ThreadPoolExecutor(jobs + 1) as ex:
+        binding = ex.submit(_compile_binding, force)
         results = list(ex.map(lambda s: _compile(nvcc, s, force, verbose), srcs))
+        binding_obj = binding.result()
     logs = [log for _, log in results if log.strip()]
     objs = [o for o, _ in results]
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
@@ -69,6 +109,7 @@ def build(jobs: int = 0, force: bool = False, verbose: bool = False) -> str:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    _link_binding(binding_obj, force)
     if verbose:
         for log in logs:
             sys.stderr.write(log)

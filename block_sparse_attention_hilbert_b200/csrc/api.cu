@@ -1127,7 +1127,7 @@ svsa_status svsa_cache_select(const svsa_cache* c, const void* q, int32_t* idx, 
   SVSA_TRY(check_query(c, p));
   if (p->cap < 1 || p->first < 0 || p->last < 0 || (long long)p->first + p->last > p->cap)
     return fail(SVSA_ERR_INVALID_ARG, "cap=%d must be >= 1 and hold first=%d and last=%d", p->cap, p->first, p->last);
-  if (c->max_blocks > 65536) return fail(SVSA_ERR_UNSUPPORTED, "max_blocks=%d exceeds 65536", c->max_blocks);
+  if (c->max_blocks > 32768) return fail(SVSA_ERR_UNSUPPORTED, "max_blocks=%d exceeds 32768", c->max_blocks);
   if (p->heads_q / c->heads > 128)
     return fail(SVSA_ERR_UNSUPPORTED, "%d query heads per key head exceed 128", p->heads_q / c->heads);
   SVSA_PTR(q, "q");

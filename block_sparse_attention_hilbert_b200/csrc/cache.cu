@@ -16,9 +16,9 @@
 //   times a power of two, exact in fp32, so that no list depends on the order
 //   of a sum and equal scores are really equal (the lower index wins).  Each
 //   CTA scores a range of blocks, one thread per block (its mean is one
-//   128-byte line), and keeps the sortable keys in shared memory; the cap-th
-//   largest key is found by four 8-bit digits with histograms summed over
-//   the cluster, and the list is written in ascending order.
+//   128-byte line), and puts the sortable keys into the first CTA's shared
+//   memory; that one finds the cap-th largest key by three digits of 11, 11
+//   and 10 bits and writes the list in ascending order.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
@@ -252,23 +252,40 @@ struct SelectArgs {
   int32_t* idx;                    // [B][Tq][heads][cap]
   int32_t* cnt;                    // [B][Tq][heads]
   int heads_q, Tq, causal, cap, first, last;
-  int chunk;                       // blocks of a CTA at most
 };
 
+constexpr int kBins = 2048;
+
+// Inclusive sums over the CTA's threads of two counts at once (each below 2^16).
+__device__ __forceinline__ uint32_t scan_pairs(uint32_t v, uint32_t* warp_tot) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_tot[warp] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) v += warp_tot[w];
+  return v;
+}
+
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) cache_select_kernel(const __grid_constant__ SelectArgs p) {
+__global__ void __launch_bounds__(kThreads, 5) cache_select_kernel(const __grid_constant__ SelectArgs p) {
   extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ int hist[4][256];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t warp_tot[2][kWarps];
   __shared__ int found[2];
-  __shared__ int counts[2];        // keys above and at the threshold, read by the cluster
-  __shared__ int wsum[2][kWarps];
-  __shared__ int warp_tot[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  // (arrive now, wait before the first write into another CTA's shared memory: it has started by then)
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   const int group = p.heads_q / p.c.heads;
-  uint32_t* keys = smem;                                   // [chunk]
-  uint32_t* qc = smem + (p.chunk + 3) / 4 * 4;             // [group][D / 4]
+  uint32_t* qc = smem;                                     // [group][D / 4]
   float* qs = reinterpret_cast<float*>(qc + group * (D / 4));
+  uint32_t* keys = smem + (group * (D / 4 + 1) + 3) / 4 * 4;          // [max_blocks], used in the first CTA
 
   long long row = blockIdx.x / C;
   const int h = (int)(row % p.c.heads);
@@ -278,30 +295,28 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const __grid_con
   int32_t* idx = p.idx + out_row * p.cap;
 
   const int len0 = __ldg(p.c.len + b);
-  const int len = min(max(len0, 0), p.c.max_blocks * kBlock);
-  const int seen = p.causal ? max(len - p.Tq + 1 + t, 0) : len;
-  const int nb = (seen + kBlock - 1) / kBlock;
-  if (rank == 0 && threadIdx.x == 0) {
-    p.cnt[out_row] = min(nb, p.cap);
-    if (len != len0) atomicOr(&g_cache_flags, kFlagIndex);
-  }
-  if (nb <= p.cap) {                                       // nothing to choose (uniform over the cluster)
-    for (int i = rank * kThreads + threadIdx.x; i < p.cap; i += C * kThreads) idx[i] = i < nb ? i : 0;
-    return;
-  }
-  const int per = (nb + C - 1) / C;
-  const int lo = min(rank * per, nb), n = min(lo + per, nb) - lo;
-
-  // the group's queries in 8 bits
+  // the group's queries in 8 bits, a warp each
   for (int g = threadIdx.x / 32; g < group; g += kWarps) {
-    const T* q = static_cast<const T*>(p.q) + (((long long)b * p.heads_q + h * group + g) * p.Tq + t) * D;
     const int lane = threadIdx.x % 32;
+    const char* q = static_cast<const char*>(p.q) + (((long long)b * p.heads_q + h * group + g) * p.Tq + t) * (2LL * D);
     float v[D / 32];
+    if constexpr (D == 128) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(q) + lane);
+      float x[8];
+      unpack8<T>(make_uint4(w.x, w.y, 0u, 0u), x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = x[e];
+    } else {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q) + lane);
+      float x[8];
+      unpack8<T>(make_uint4(w, 0u, 0u, 0u), x);
+      v[0] = x[0];
+      v[1] = x[1];
+    }
     float amax = 0.f;
     bool odd = false;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) {
-      v[e] = (float)q[lane * (D / 32) + e];
       const float a = fabsf(v[e]);
       if (a < INFINITY) amax = fmaxf(amax, a);
       else odd = true;
@@ -315,143 +330,134 @@ __global__ void __launch_bounds__(kThreads) cache_select_kernel(const __grid_con
     else reinterpret_cast<uint16_t*>(qc + g * (D / 4))[lane] = (uint16_t)w;
     if (lane == 0) qs[g] = s;
   }
-  for (int i = threadIdx.x; i < 4 * 256; i += kThreads) hist[i / 256][i % 256] = 0;
-  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0u;
 
+  const int len = min(max(len0, 0), p.c.max_blocks * kBlock);
+  const int seen = p.causal ? max(len - p.Tq + 1 + t, 0) : len;
+  const int nb = (seen + kBlock - 1) / kBlock;
+  if (rank == 0 && threadIdx.x == 0) {
+    p.cnt[out_row] = min(nb, p.cap);
+    if (len != len0) atomicOr(&g_cache_flags, kFlagIndex);
+  }
+  if (nb <= p.cap) {                                       // nothing to choose (uniform over the cluster)
+    for (int i = rank * kThreads + threadIdx.x; i < p.cap; i += C * kThreads) idx[i] = i < nb ? i : 0;
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+    return;
+  }
+  __syncthreads();
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+  uint32_t* to = C > 1 ? cluster.map_shared_rank(keys, 0) : keys;
+  // A warp scores 32 blocks at a time, one per lane in the end; D / 16 lanes
+  // read a mean together (whole lines), each a 16-byte piece of as many
+  // blocks, and an exchange in halves leaves every lane its block's sum.
+  constexpr int L = D / 16;
+  const int lane = threadIdx.x % 32, e = lane % L;
   bool bad = false;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int j = lo + i;
-    uint32_t key = 0u;
-    if (j < p.first || j >= nb - p.last) {
-      key = 0xffffffffu;
-    } else {
-      const int page = __ldg(p.c.table + (long long)b * p.c.max_blocks + j);
-      if ((unsigned)page >= (unsigned)p.c.n_pages) {
-        bad = true;
-      } else {
-        const long long cell = (long long)page * p.c.heads + h;
-        const uint4* mp = reinterpret_cast<const uint4*>(p.c.mean + cell * D);
-        uint4 m[D / 16];
+  const int32_t* pages = p.c.table + (long long)b * p.c.max_blocks;
+  const int step = C * kThreads;
+  int j = rank * kThreads + threadIdx.x;
+  int page = j < nb ? __ldg(pages + j) : 0;
+  for (; j - lane < nb; j += step) {                        // uniform over the warp
+    const int next = j + step < nb ? __ldg(pages + j + step) : 0;
+    const bool forced = j < p.first || j >= nb - p.last;
+    const bool ok = j < nb && (unsigned)page < (unsigned)p.c.n_pages;
+    const int cell = ok ? page * p.c.heads + h : h;         // (page 0 in the place of one that is not there)
+    const float ms = __ldg(p.c.mean_scale + cell);
+    uint4 m[L];
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) m[e] = __ldg(mp + e);
-        const float ms = __ldg(p.c.mean_scale + cell);
-        float best = -INFINITY;
-        for (int g = 0; g < group; ++g) {
-          const uint4* qg = reinterpret_cast<const uint4*>(qc + g * (D / 4));
-          int dot = 0;
-#pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            const uint4 a = qg[e];
-            dot = __dp4a((int)a.x, (int)m[e].x, dot);
-            dot = __dp4a((int)a.y, (int)m[e].y, dot);
-            dot = __dp4a((int)a.z, (int)m[e].z, dot);
-            dot = __dp4a((int)a.w, (int)m[e].w, dot);
-          }
-          best = fmaxf(best, (float)dot * (qs[g] * ms));
-        }
-        const uint32_t u = __float_as_uint(best + 0.f);     // -0 becomes +0
-        key = (u & 0x80000000u) ? ~u : u | 0x80000000u;
-      }
+    for (int i = 0; i < L; ++i) {
+      const int c = __shfl_sync(0xffffffffu, cell, lane - e + i);
+      m[i] = __ldg(reinterpret_cast<const uint4*>(p.c.mean + (long long)c * D) + e);
     }
-    keys[i] = key;
-    atomicAdd(&hist[0][key >> 24], 1);
+    float best = -INFINITY;
+    for (int g = 0; g < group; ++g) {
+      const uint4 a = reinterpret_cast<const uint4*>(qc + g * (D / 4))[e];
+      int dot[L];
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        dot[i] = __dp4a((int)a.x, (int)m[i].x, 0);
+        dot[i] = __dp4a((int)a.y, (int)m[i].y, dot[i]);
+        dot[i] = __dp4a((int)a.z, (int)m[i].z, dot[i]);
+        dot[i] = __dp4a((int)a.w, (int)m[i].w, dot[i]);
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) {
+        const bool up = e & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const int give = up ? dot[i] : dot[i + o], keep = up ? dot[i + o] : dot[i];
+          dot[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      best = fmaxf(best, (float)dot[0] * (qs[g] * ms));
+    }
+    if (j < nb) {
+      const uint32_t u = __float_as_uint(best + 0.f);       // -0 becomes +0
+      bad = bad || (!ok && !forced);
+      to[j] = forced ? 0xffffffffu : !ok ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    }
+    page = next;
   }
   if (bad) atomicOr(&g_cache_flags, kFlagIndex);
+  if (C > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  } else {
+    __syncthreads();
+  }
 
-  // the cap-th largest key: four digits, each from the cluster's summed histogram
+  // the cap-th largest key, digit by digit
   uint32_t prefix = 0u;
   int need = p.cap;
-#pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    if (pass > 0) {
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t key = keys[i];
-        if ((key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[pass][(key >> shift) & 255u], 1);
-      }
-    }
-    if (C > 1) cluster.sync();
-    else __syncthreads();
-    // thread t holds bin 255 - t; an inclusive scan over the threads counts the keys from the top
-    const int bin = 255 - threadIdx.x;
-    int c = 0;
-    for (int r = 0; r < C; ++r) c += C > 1 ? cluster.map_shared_rank(&hist[pass][0], r)[bin] : hist[pass][bin];
-    int up = c;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, up, o);
-      if ((threadIdx.x & 31) >= o) up += v;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 0 : pass == 1 ? 21 : 10;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    for (int i = threadIdx.x; i < nb; i += kThreads) {
+      const uint32_t key = keys[i];
+      if (pass == 0 || (key >> above) == (prefix >> above)) atomicAdd(&hist[(key >> shift) & mask], 1u);
     }
-    if ((threadIdx.x & 31) == 31) warp_tot[threadIdx.x / 32] = up;
     __syncthreads();
-    for (int w = 0; w < (int)threadIdx.x / 32; ++w) up += warp_tot[w];
-    if (up >= need && up - c < need) {
-      found[0] = bin;
-      found[1] = need - (up - c);
+    // thread i holds the eight bins below 2048 - 8 i; the scan counts the keys from the top
+    uint32_t c[8], sum = 0u;
+    uint4* mine = reinterpret_cast<uint4*>(hist + kBins - 8 - 8 * threadIdx.x);
+    const uint4 lo = mine[0], hi = mine[1];
+    c[0] = hi.w; c[1] = hi.z; c[2] = hi.y; c[3] = hi.x;
+    c[4] = lo.w; c[5] = lo.z; c[6] = lo.y; c[7] = lo.x;
+    mine[0] = mine[1] = make_uint4(0u, 0u, 0u, 0u);         // clear for the next digit
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += c[e];
+    uint32_t up = scan_pairs(sum, warp_tot[pass & 1]);
+    if (up >= (uint32_t)need && up - sum < (uint32_t)need) {
+      int at = (int)(up - sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (at < need && at + (int)c[e] >= need) {
+          found[0] = kBins - 1 - 8 * (int)threadIdx.x - e;
+          found[1] = need - at;
+        }
+        at += (int)c[e];
+      }
     }
     __syncthreads();
     prefix |= (uint32_t)found[0] << shift;
     need = found[1];
   }
 
-  // keys above the threshold, and the first `need` equal to it
-  int above = 0, equal = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    above += keys[i] > prefix;
-    equal += keys[i] == prefix;
-  }
-  above = __reduce_add_sync(0xffffffffu, above);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (threadIdx.x % 32 == 0) {
-    wsum[0][threadIdx.x / 32] = above;
-    wsum[1][threadIdx.x / 32] = equal;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    int s = 0;
-    for (int w = 0; w < kWarps; ++w) s += wsum[threadIdx.x][w];
-    counts[threadIdx.x] = s;
-  }
-  if (C > 1) cluster.sync();
-  else __syncthreads();
-  int taken = 0, ties = 0;                                  // before this CTA's range
-  for (int r = 0; r < rank; ++r) {
-    const int* o = cluster.map_shared_rank(&counts[0], r);
-    taken += o[0];
-    ties += o[1];
-  }
-  if (C > 1) cluster.sync();                                // no CTA leaves while another reads its counts
-  taken += min(ties, need);
-  for (int base = 0; base < n; base += kThreads) {
-    const int i = base + threadIdx.x;
-    const uint32_t key = i < n ? keys[i] : 0u;
-    const bool eq = i < n && key == prefix, gt = i < n && key > prefix;
-    const unsigned lanes = (1u << (threadIdx.x & 31)) - 1u;
-    const unsigned beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) {
-      wsum[0][threadIdx.x / 32] = __popc(bgt);
-      wsum[1][threadIdx.x / 32] = __popc(beq);
-    }
-    __syncthreads();
-    int g0 = 0, e0 = 0, gall = 0, eall = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int a = wsum[0][w], e = wsum[1][w];
-      if (w < (int)threadIdx.x / 32) {
-        g0 += a;
-        e0 += e;
-      }
-      gall += a;
-      eall += e;
-    }
-    const int eq_before = ties + e0 + __popc(beq & lanes);
-    const int gt_before = g0 + __popc(bgt & lanes);
-    // `taken` counts what lies before this tile; ties of this tile that are taken
-    const int tile_ties_before = min(eq_before, need) - min(ties, need);
-    if (gt || (eq && eq_before < need)) idx[taken + gt_before + tile_ties_before] = lo + i;
-    taken += gall + min(ties + eall, need) - min(ties, need);
-    ties += eall;
+  // the keys above it, and the first `need` equal to it, in order; a thread
+  // takes consecutive keys (an odd number: no bank conflicts)
+  const int per = ((nb + kThreads - 1) / kThreads) | 1;
+  const int lo = min((int)threadIdx.x * per, nb), hi = min(lo + per, nb);
+  uint32_t mine = 0u;                                       // equal << 16 | above
+  for (int i = lo; i < hi; ++i) mine += keys[i] > prefix ? 1u : keys[i] == prefix ? 0x10000u : 0u;
+  const uint32_t upto = scan_pairs(mine, warp_tot[1]) - mine;
+  int gt = (int)(upto & 0xffffu), eq = (int)(upto >> 16);
+  for (int i = lo; i < hi; ++i) {
+    const uint32_t key = keys[i];
+    if (key > prefix || (key == prefix && eq < need)) idx[gt + min(eq, need)] = i;
+    gt += key > prefix;
+    eq += key == prefix;
   }
 }
 
@@ -508,13 +514,11 @@ cudaError_t launch_cache_select(const CacheArgs& c, const void* q, int heads_q, 
   p.last = last;
   const long long rows = (long long)c.B * Tq * c.heads;
   // CTAs per row: more while a CTA keeps at least one block per thread and the
-  // grid stays within a few CTAs per SM; and enough for the keys to fit
+  // grid stays within a few CTAs per SM
   int C = 1;
   while (C < 8 && c.max_blocks > C * kThreads && rows * C < kNumSMs * 4) C *= 2;
-  while (C < 8 && ceil_div(c.max_blocks, C) > 16384) C *= 2;
-  p.chunk = ceil_div(c.max_blocks, C);
   const int group = heads_q / c.heads;
-  const size_t smem = (size_t)((p.chunk + 3) / 4 * 4) * 4 + (size_t)group * (c.d + 4);
+  const size_t smem = ((size_t)(group * (c.d / 4 + 1) + 3) / 4 * 4 + c.max_blocks) * 4;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kThreads);

@@ -599,7 +599,7 @@ typedef struct {
  * in 127; up to cap in all, equal scores by the lower index.  Dot products of
  * whole numbers are exact, so the lists depend on nothing but the inputs.
  * idx [B, Tq, heads, cap]: ascending, then zeros; cnt [B, Tq, heads].
- * first + last <= cap; max_blocks <= 65536; heads_q / heads <= 128; mean and
+ * first + last <= cap; max_blocks <= 32768; heads_q / heads <= 128; mean and
  * mean_scale required.  A value of q that is not finite saturates (NaN counts
  * 0) and is reported as SVSA_ERR_RANGE. */
 svsa_status svsa_cache_select(const svsa_cache* c, const void* q, int32_t* idx, int32_t* cnt,

@@ -157,7 +157,7 @@ def test_select_and_attention_reject():
     assert _attn(c, _query(Tq=1 << 25)) == 2
     for bad in (dict(cap=0), dict(first=-1), dict(last=-1), dict(first=2, last=2)):
         assert _select(c, _query(**bad)) == 1, bad
-    assert _select(_cache(max_blocks=65537), _query()) == 2
+    assert _select(_cache(max_blocks=32769), _query()) == 2
     assert _select(c, _query(heads_q=2 * 129)) == 2
     for bad in (dict(q=None), dict(idx=None), dict(cnt=None), dict(q=145)):
         assert _select(c, _query(), **bad) == 1, bad

@@ -1098,7 +1098,7 @@ svsa_status svsa_cache_append(const svsa_cache* c, const void* k, const void* v,
   if (p->dtype != SVSA_BF16 && p->dtype != SVSA_F16) return fail(SVSA_ERR_UNSUPPORTED, "dtype=%d unknown", p->dtype);
   SVSA_TRY(check_strides(p->k_stride, "k_stride"));
   SVSA_TRY(check_strides(p->v_stride, "v_stride"));
-  if (((long long)p->N / kBlock + 2) * c->heads * c->B >= (1LL << 31))
+  if (((long long)p->N / kBlock + 2) * c->heads * c->B >= (1LL << 30))
     return fail(SVSA_ERR_UNSUPPORTED, "too many blocks for one call");
   SVSA_PTR(k, "k");
   SVSA_PTR(v, "v");

@@ -1,12 +1,13 @@
 // The 8-bit block cache: appending tokens, and choosing blocks for queries.
 //
 // cache_append_kernel  one CTA per (sequence, head, block that receives
-//   tokens).  For K and V: amax of the new rows, the block's scale = the
-//   larger of what it had and the smallest power of two that holds amax; the
-//   codes of rows that were there are rounded again only when the scale grew.
-//   Then the block's key mean from the codes: in units of the code's last
-//   place (1 for int8, 2^-9 for e4m3) the column sums are whole numbers below
-//   2^24, so the mean does not depend on the order of the sum.
+//   tokens), keys and values apart.  amax of the new rows; the block's scale =
+//   the larger of what it had and the smallest power of two that holds amax;
+//   the codes of rows that were there are rounded again only when the scale
+//   grew.  Then, for keys, the block's mean from the codes: all of them are
+//   multiples of the code's last place (1 for int8, 2^-9 for e4m3) and the
+//   column sums stay below 2^24 of those, so fp32 sums are exact and the mean
+//   does not depend on their order.
 //   Bound by HBM for long appends (4 bytes read and 2 written per key and
 //   value pair, in 16- and 8-byte pieces), by launch latency for one token.
 //
@@ -72,21 +73,46 @@ __device__ __forceinline__ uint32_t encode(float y) {
   }
 }
 
-// A code as a whole number of its last places: int8 itself; e4m3 in units of
-// 2^-9, (m or 8 + m) << (e - 1), below 2^18.
+// Eight codes of values that are not NaN, and the codes' values (in units of
+// 1 for int8, as they are for e4m3) added to `total`.
 template <bool I8>
-__device__ __forceinline__ int decode_units(uint32_t c) {
-  if constexpr (I8) {
-    return (int)(int8_t)c;
-  } else {
-    const int e = (c >> 3) & 15, m = c & 7;
-    const int v = e ? (8 + m) << (e - 1) : m;
-    return (c & 0x80u) ? -v : v;
+__device__ __forceinline__ uint2 encode8(const float y[8]) {
+  uint32_t c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (I8) {
+      int v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __float2int_rn(fminf(fmaxf(y[4 * i + e], -127.f), 127.f));
+      c[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
+    } else {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i], y[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2], y[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+      c[i] = lo | hi << 16;
+    }
   }
+  return make_uint2(c[0], c[1]);
 }
 
 template <bool I8>
-constexpr float unit() { return I8 ? 1.f : 1.f / 512.f; }
+__device__ __forceinline__ void decode8(uint2 code, float x[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? code.y : code.x;
+    if constexpr (I8) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * i + e] = (float)(int8_t)(w >> (8 * e));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * e)), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+        x[4 * i + 2 * e] = f.x;
+        x[4 * i + 2 * e + 1] = f.y;
+      }
+    }
+  }
+}
 
 struct AppendArgs {
   CacheArgs c;
@@ -98,23 +124,26 @@ struct AppendArgs {
 };
 
 template <int D, typename T, bool I8>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const __grid_constant__ AppendArgs p) {
   constexpr int L = D / 8;                 // lanes per row
   constexpr int R = kThreads / L;          // rows per pass
   constexpr int P = kBlock / R;            // passes: 4 (d = 128) or 2 (d = 64)
-  __shared__ float wmax[2][kWarps];
-  __shared__ int sums[R][D];
+  constexpr float kUnit = I8 ? 1.f : 1.f / 512.f;          // the codes' last place
+  __shared__ float wmax[kWarps], wtop[kWarps];
+  __shared__ float sums[R][D];
   const int ch = threadIdx.x % L, rl = threadIdx.x / L;
-  long long blk_id = blockIdx.x;
-  const int x = (int)(blk_id % p.wide);
-  blk_id /= p.wide;
-  const int h = (int)(blk_id % p.c.heads), b = (int)(blk_id / p.c.heads);
+  unsigned id = blockIdx.x;
+  const int w = (int)(id & 1u);            // keys or values
+  id >>= 1;
+  const int x = (int)(id % p.wide);
+  id /= p.wide;
+  const int h = (int)(id % p.c.heads), b = (int)(id / p.c.heads);
 
   const int room = p.c.max_blocks * kBlock;
   const int len0 = __ldg(p.c.len + b), new0 = p.n_new ? __ldg(p.n_new + b) : p.N;
   const int len = min(max(len0, 0), room);
   const int n_new = min(min(max(new0, 0), p.N), room - len);
-  if (x == 0 && h == 0 && threadIdx.x == 0) {
+  if (x == 0 && h == 0 && w == 0 && threadIdx.x == 0) {
     if (len != len0 || n_new != new0) atomicOr(&g_cache_flags, kFlagIndex);
     if (p.len_out) p.len_out[b] = len + n_new;
   }
@@ -128,119 +157,111 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   }
   const int had = lo - j * kBlock, end = hi - j * kBlock;   // rows [had, end) of the block are new
   const long long cell = (long long)page * p.c.heads + h;
-  uint8_t* codes[2] = {static_cast<uint8_t*>(p.c.k) + cell * (kBlock * D), static_cast<uint8_t*>(p.c.v) + cell * (kBlock * D)};
-  float* scales[2] = {p.c.k_scale + cell, p.c.v_scale + cell};
+  uint8_t* codes = static_cast<uint8_t*>(w ? p.c.v : p.c.k) + cell * (kBlock * D) + ch * 8;
+  float* scale_at = (w ? p.c.v_scale : p.c.k_scale) + cell;
+  const bool mean_too = w == 0 && p.c.mean != nullptr;
 
-  uint4 raw[2][P];
-  float amax[2] = {0.f, 0.f};
+  // a new row's eight values, or an old row's eight codes
+  uint4 raw[P];
+  const char* src = static_cast<const char*>(p.x[w]) +
+                    2 * ((long long)b * p.stride[w][0] + (long long)h * p.stride[w][1]) + ch * 16;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int r = rl + R * i;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= had && r < end) {
+      raw[i] = *reinterpret_cast<const uint4*>(src + 2 * (long long)(j * kBlock + r - len) * p.stride[w][2]);
+    } else if (r < had && mean_too) {
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + r * D);
+      raw[i].x = c.x;
+      raw[i].y = c.y;
+    }
+  }
+  const float start = had > 0 ? *scale_at : 0.f;
+  float amax = 0.f;
   bool odd = false;
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const char* src = static_cast<const char*>(p.x[w]) +
-                      2 * ((long long)b * p.stride[w][0] + (long long)h * p.stride[w][1]) + ch * 16;
+  for (int i = 0; i < P; ++i) {
+    if (rl + R * i < had) continue;
+    float v[8];
+    unpack8<T>(raw[i], v);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int r = rl + R * i;
-      raw[w][i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r >= had && r < end)
-        raw[w][i] = *reinterpret_cast<const uint4*>(src + 2 * (long long)(j * kBlock + r - len) * p.stride[w][2]);
+    for (int e = 0; e < 8; ++e) {
+      const float a = fabsf(v[e]);
+      if (a < INFINITY) amax = fmaxf(amax, a);
+      else odd = true;
     }
   }
-  float start[2];
-  start[0] = had > 0 ? *scales[0] : 0.f;
-  start[1] = had > 0 ? *scales[1] : 0.f;
+  if (odd) atomicOr(&g_cache_flags, kFlagNotFinite);
+  amax = warp_max(amax);
+  if (threadIdx.x % 32 == 0) wmax[threadIdx.x / 32] = amax;
+  __syncthreads();                                     // also: every thread has read the old scale
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
+  for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, wmax[i]);
+  const float scale = fmaxf(start, pow2_scale(amax, I8));
+  const float inv = scale > 0.f ? 1.f / scale : 0.f;
+  if (threadIdx.x == 0) *scale_at = scale;
+  const bool grew = had > 0 && scale != start;
+  const float back = grew ? start / scale : 1.f;
+
+  float total[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+  for (int i = 0; i < P; ++i) {
+    const int r = rl + R * i;
+    uint2* at = reinterpret_cast<uint2*>(codes + r * D);
+    uint2 c;
+    if (r >= end) continue;
+    if (r >= had) {
       float v[8];
-      unpack8<T>(raw[w][i], v);
+      unpack8<T>(raw[i], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float a = fabsf(v[e]);
-        if (a < INFINITY) amax[w] = fmaxf(amax[w], a);
-        else odd = true;
+        // (what is not finite: NaN gives 0, an infinity the largest code, and 0 under the scale 0)
+        if (odd && !(fabsf(v[e]) < INFINITY)) v[e] = v[e] != v[e] ? 0.f : copysignf(3.4e38f, v[e]);
+        v[e] *= inv;
       }
-    }
-  if (odd) atomicOr(&g_cache_flags, kFlagNotFinite);
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    amax[w] = warp_max(amax[w]);
-    if (threadIdx.x % 32 == 0) wmax[w][threadIdx.x / 32] = amax[w];
-  }
-  __syncthreads();                                     // also: every thread has read the old scales
-  float scale[2], inv[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    float m = wmax[w][0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) m = fmaxf(m, wmax[w][i]);
-    scale[w] = fmaxf(start[w], pow2_scale(m, I8));
-    inv[w] = scale[w] > 0.f ? 1.f / scale[w] : 0.f;
-  }
-  if (threadIdx.x < 2) *scales[threadIdx.x] = threadIdx.x ? scale[1] : scale[0];
-
-  int total[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const bool grew = had > 0 && scale[w] != start[w];
-    const float back = grew ? start[w] / scale[w] : 1.f;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int r = rl + R * i;
-      uint2* at = reinterpret_cast<uint2*>(codes[w] + (long long)r * D + ch * 8);
-      uint32_t c[2] = {0u, 0u};
-      if (r >= had && r < end) {
+      c = encode8<I8>(v);
+      *at = c;
+    } else {
+      if (!grew && !mean_too) continue;
+      c = mean_too ? make_uint2(raw[i].x, raw[i].y) : *at;
+      if (grew) {
         float v[8];
-        unpack8<T>(raw[w][i], v);
+        decode8<I8>(c, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e / 4] |= encode<I8>(v[e] * inv[w]) << (8 * (e % 4));
-        *at = make_uint2(c[0], c[1]);
-      } else if (r < had && (grew || w == 0)) {
-        const uint2 old = *at;
-        c[0] = old.x;
-        c[1] = old.y;
-        if (grew) {
-          uint32_t n[2] = {0u, 0u};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t was = (c[e / 4] >> (8 * (e % 4))) & 0xffu;
-            uint32_t now = encode<I8>((float)decode_units<I8>(was) * unit<I8>() * back);
-            if (!I8) now |= was & 0x80u;                    // -0 keeps its sign
-            n[e / 4] |= now << (8 * (e % 4));
-          }
-          c[0] = n[0];
-          c[1] = n[1];
-          *at = make_uint2(c[0], c[1]);
-        }
-      }
-      if (w == 0 && r < end) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) total[e] += decode_units<I8>((c[e / 4] >> (8 * (e % 4))) & 0xffu);
+        for (int e = 0; e < 8; ++e) v[e] = v[e] == v[e] ? v[e] * back : 0.f;
+        c = encode8<I8>(v);
+        *at = c;
       }
     }
-  }
-  if (p.c.mean == nullptr) return;
+    if (mean_too) {
+      float v[8];
+      decode8<I8>(c, v);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[rl][ch * 8 + e] = total[e];
+      for (int e = 0; e < 8; ++e) total[e] += v[e];
+    }
+  }
+  if (!mean_too) return;
+  *reinterpret_cast<float4*>(&sums[rl][ch * 8]) = make_float4(total[0], total[1], total[2], total[3]);
+  *reinterpret_cast<float4*>(&sums[rl][ch * 8 + 4]) = make_float4(total[4], total[5], total[6], total[7]);
   __syncthreads();
   float mean = 0.f;
   if (threadIdx.x < D) {
-    int t = 0;
+    float t = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) t += sums[r][threadIdx.x];
-    mean = __fdiv_rn((float)t, (float)end);
+    mean = __fdiv_rn(t * (1.f / kUnit), (float)end);
   }
   const float m = warp_max(fabsf(mean));
-  if (threadIdx.x < D && threadIdx.x % 32 == 0) wmax[1][threadIdx.x / 32] = m;    // (the barrier above parts it from the reads)
+  if (threadIdx.x % 32 == 0) wtop[threadIdx.x / 32] = m;
   __syncthreads();
   if (threadIdx.x < D) {
-    float top = wmax[1][0];
+    float top = wtop[0];
 #pragma unroll
-    for (int i = 1; i < D / 32; ++i) top = fmaxf(top, wmax[1][i]);
+    for (int i = 1; i < D / 32; ++i) top = fmaxf(top, wtop[i]);
     const float s = pow2_scale(top, true);
     p.c.mean[cell * D + threadIdx.x] = (int8_t)encode<true>(s > 0.f ? mean / s : 0.f);
-    if (threadIdx.x == 0) p.c.mean_scale[cell] = s * unit<I8>() * scale[0];
+    if (threadIdx.x == 0) p.c.mean_scale[cell] = s * kUnit * scale;
   }
 }
 
@@ -489,7 +510,7 @@ cudaError_t launch_cache_append(const CacheArgs& c, const void* k, const void* v
   p.N = N;
   // N tokens touch at most ceil((N - 1) / 64) + 1 blocks, wherever they start
   p.wide = (N + kBlock - 2) / kBlock + 1;
-  const unsigned grid = (unsigned)((long long)p.wide * c.heads * c.B);
+  const unsigned grid = (unsigned)((long long)p.wide * c.heads * c.B * 2);
   by_d_type(c.d, f16, [&](auto D_, auto z) {
     constexpr int D = decltype(D_)::value;
     using T = decltype(z);

@@ -50,6 +50,12 @@ __device__ __forceinline__ void unpack8<__nv_bfloat16>(uint4 v, float x[8]) {
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
+template <typename T>
+struct Pair2;
+template <>
+struct Pair2<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <>
+struct Pair2<__half> { using type = __half2; };
 template <>
 __device__ __forceinline__ void unpack8<__half>(uint4 v, float x[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -73,19 +79,33 @@ __device__ __forceinline__ uint32_t encode(float y) {
   }
 }
 
-// Eight codes of values that are not NaN, and the codes' values (in units of
-// 1 for int8, as they are for e4m3) added to `total`.
+// max |x| of packed pairs, NaN and infinities kept.
+__device__ __forceinline__ __nv_bfloat162 abs_max(__nv_bfloat162 m, uint32_t w) {
+  w &= 0x7fff7fffu;
+  return __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+__device__ __forceinline__ __half2 abs_max(__half2 m, uint32_t w) {
+  w &= 0x7fff7fffu;
+  return __hmax2_nan(m, *reinterpret_cast<const __half2*>(&w));
+}
+
+// Eight codes of x * inv, |x * inv| within the codes.  For int8, adding 1.5 *
+// 2^23 leaves the rounded value in the low byte (the product by a power of two
+// is exact, so the one rounding is that of the sum).
 template <bool I8>
-__device__ __forceinline__ uint2 encode8(const float y[8]) {
+__device__ __forceinline__ uint2 encode8(const float x[8], float inv) {
   uint32_t c[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if constexpr (I8) {
-      int v[4];
+      uint32_t v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __float2int_rn(fminf(fmaxf(y[4 * i + e], -127.f), 127.f));
+      for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(fmaf(x[4 * i + e], inv, 12582912.f));
       c[i] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
     } else {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[4 * i + e] = x[4 * i + e] * inv;
       const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i], y[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
       const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * i + 2], y[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
       c[i] = lo | hi << 16;
@@ -178,26 +198,42 @@ __global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const __grid_
     }
   }
   const float start = had > 0 ? *scale_at : 0.f;
-  float amax = 0.f;
-  bool odd = false;
+  // max |x| of the new rows in their own type, exactly; where it is not finite
+  // (rare), once more over the values that are
+  float amax;
+  {
+    using T2 = typename Pair2<T>::type;
+    const uint32_t zero = 0u;
+    T2 m = *reinterpret_cast<const T2*>(&zero);
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    if (rl + R * i < had) continue;
+    for (int i = 0; i < P; ++i)
+      if (rl + R * i >= had) m = abs_max(abs_max(abs_max(abs_max(m, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
     float v[8];
-    unpack8<T>(raw[i], v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = fabsf(v[e]);
-      if (a < INFINITY) amax = fmaxf(amax, a);
-      else odd = true;
-    }
+    unpack8<T>(make_uint4(*reinterpret_cast<uint32_t*>(&m), 0u, 0u, 0u), v);
+    amax = v[0] != v[0] || v[1] != v[1] ? INFINITY : fmaxf(v[0], v[1]);
   }
-  if (odd) atomicOr(&g_cache_flags, kFlagNotFinite);
-  amax = warp_max(amax);
-  if (threadIdx.x % 32 == 0) wmax[threadIdx.x / 32] = amax;
-  __syncthreads();                                     // also: every thread has read the old scale
+  auto reduce = [&](float m) {
+    m = warp_max(m);
+    if (threadIdx.x % 32 == 0) wmax[threadIdx.x / 32] = m;
+    __syncthreads();                                   // also: every thread has read the old scale
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, wmax[i]);
+    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, wmax[i]);
+    return m;
+  };
+  amax = reduce(amax);
+  const bool odd = !(amax < INFINITY);                 // uniform over the CTA
+  if (odd) {
+    if (threadIdx.x == 0) atomicOr(&g_cache_flags, kFlagNotFinite);
+    __syncthreads();
+    amax = 0.f;
+    for (int i = 0; i < P; ++i) {
+      float v[8];
+      unpack8<T>(raw[i], v);
+      for (int e = 0; e < 8; ++e)
+        if (rl + R * i >= had && fabsf(v[e]) < INFINITY) amax = fmaxf(amax, fabsf(v[e]));
+    }
+    amax = reduce(amax);
+  }
   const float scale = fmaxf(start, pow2_scale(amax, I8));
   const float inv = scale > 0.f ? 1.f / scale : 0.f;
   if (threadIdx.x == 0) *scale_at = scale;
@@ -214,13 +250,12 @@ __global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const __grid_
     if (r >= had) {
       float v[8];
       unpack8<T>(raw[i], v);
+      if (odd) {                                       // NaN gives 0, an infinity the largest code (0 under the scale 0)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // (what is not finite: NaN gives 0, an infinity the largest code, and 0 under the scale 0)
-        if (odd && !(fabsf(v[e]) < INFINITY)) v[e] = v[e] != v[e] ? 0.f : copysignf(3.4e38f, v[e]);
-        v[e] *= inv;
+        for (int e = 0; e < 8; ++e)
+          if (!(fabsf(v[e]) < INFINITY)) v[e] = v[e] != v[e] ? 0.f : copysignf((I8 ? 127.f : 448.f) * scale, v[e]);
       }
-      c = encode8<I8>(v);
+      c = encode8<I8>(v, inv);
       *at = c;
     } else {
       if (!grew && !mean_too) continue;
@@ -229,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const __grid_
         float v[8];
         decode8<I8>(c, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] == v[e] ? v[e] * back : 0.f;
-        c = encode8<I8>(v);
+        for (int e = 0; e < 8; ++e) v[e] = v[e] == v[e] ? v[e] : 0.f;
+        c = encode8<I8>(v, back);
         *at = c;
       }
     }

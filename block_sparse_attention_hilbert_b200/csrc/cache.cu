@@ -143,13 +143,18 @@ struct AppendArgs {
   int N, wide;                     // wide: blocks that N tokens can touch
 };
 
+// (half as many threads as rows x lanes would want: what a thread does once per
+// block, indices, the maximum and the scale, then weighs half as much)
+constexpr int kAppendThreads = 128;
+
 template <int D, typename T, bool I8>
-__global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const __grid_constant__ AppendArgs p) {
+__global__ void __launch_bounds__(kAppendThreads, 7) cache_append_kernel(const __grid_constant__ AppendArgs p) {
   constexpr int L = D / 8;                 // lanes per row
-  constexpr int R = kThreads / L;          // rows per pass
-  constexpr int P = kBlock / R;            // passes: 4 (d = 128) or 2 (d = 64)
+  constexpr int R = kAppendThreads / L;    // rows per pass
+  constexpr int P = kBlock / R;            // passes: 8 (d = 128) or 4 (d = 64)
+  constexpr int W = kAppendThreads / 32;
   constexpr float kUnit = I8 ? 1.f : 1.f / 512.f;          // the codes' last place
-  __shared__ float wmax[kWarps], wtop[kWarps];
+  __shared__ float wmax[W], wtop[W];
   __shared__ float sums[R][D];
   const int ch = threadIdx.x % L, rl = threadIdx.x / L;
   unsigned id = blockIdx.x;
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 4) cache_append_kernel(const __grid_
     if (threadIdx.x % 32 == 0) wmax[threadIdx.x / 32] = m;
     __syncthreads();                                   // also: every thread has read the old scale
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, wmax[i]);
+    for (int i = 0; i < W; ++i) m = fmaxf(m, wmax[i]);
     return m;
   };
   amax = reduce(amax);
@@ -549,8 +554,8 @@ cudaError_t launch_cache_append(const CacheArgs& c, const void* k, const void* v
   by_d_type(c.d, f16, [&](auto D_, auto z) {
     constexpr int D = decltype(D_)::value;
     using T = decltype(z);
-    if (c.i8) cache_append_kernel<D, T, true><<<grid, kThreads, 0, st>>>(p);
-    else cache_append_kernel<D, T, false><<<grid, kThreads, 0, st>>>(p);
+    if (c.i8) cache_append_kernel<D, T, true><<<grid, kAppendThreads, 0, st>>>(p);
+    else cache_append_kernel<D, T, false><<<grid, kAppendThreads, 0, st>>>(p);
   });
   return cudaGetLastError();
 }

@@ -935,10 +935,8 @@ svsa_status rope_args(const svsa_norm_rope* p, NormRopeArgs* a) {
   }
   SVSA_TRY(check_strides(p->q_stride, "q_stride"));
   if (p->heads_k > 0) SVSA_TRY(check_strides(p->k_stride, "k_stride"));
-  // lane groups of one launch: at most one per (row, head)
-  if ((long long)p->B * std::max(p->rows, p->N) >= (1LL << 31) ||
-      (long long)p->B * std::max(p->rows, p->N) * ((long long)p->heads_q + p->heads_k) >= (1LL << 34))
-    return fail(SVSA_ERR_UNSUPPORTED, "too many rows for one call");
+  if ((long long)p->B * std::max(p->rows, p->N) >= (1LL << 31) || (long long)p->heads_q + p->heads_k > 32768)
+    return fail(SVSA_ERR_UNSUPPORTED, "too many rows or heads for one call");
   a->heads[0] = p->heads_q;
   a->heads[1] = p->heads_k;
   a->B = p->B;

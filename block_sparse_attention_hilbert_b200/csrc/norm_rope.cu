@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsInFlight = 4;
+constexpr int kFwdPerSM = 4, kBwdPerSM = 2;     // CTAs per SM that the registers are held to
 
 struct NormRope {
   const void* x[2];                 // q, k
@@ -161,22 +162,19 @@ __device__ __forceinline__ float group_sum(float v, unsigned mask) {
   return v;
 }
 
-// One lane group per (token, head group); item = chunk-major so that the
-// groups of a CTA write neighbouring rows of one head.
-template <int D, typename T, bool HALVES>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRope p) {
+// One lane group per (token, head group); blockIdx.y is the head group, so
+// that the groups of a CTA write neighbouring rows of one head.
+template <int D, typename T, bool HALVES, bool TURN>
+__global__ void __launch_bounds__(kThreads, kFwdPerSM) norm_rope_kernel(const __grid_constant__ NormRope p) {
   constexpr int L = D / 8;                      // lanes per row
   const int ch = threadIdx.x % L;
   const unsigned mask = (L == 32 ? ~0u : ((1u << L) - 1)) << ((threadIdx.x % 32) / L * L);
-  const long long tokens = (long long)p.B * p.rows;
-  const long long item = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-  const long long chunk_all = item / tokens;
-  if (chunk_all >= p.chunks[0] + p.chunks[1]) return;         // uniform over the lane group
-  const int which = chunk_all >= p.chunks[0];
-  const int h0 = (int)(chunk_all - (which ? p.chunks[0] : 0)) * p.hb;
+  const unsigned tok = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  if (tok >= (unsigned)(p.B * p.rows)) return;                // uniform over the lane group
+  const int which = (int)blockIdx.y >= p.chunks[0];
+  const int h0 = ((int)blockIdx.y - (which ? p.chunks[0] : 0)) * p.hb;
   const int h1 = min(h0 + p.hb, p.heads[which]);
-  const long long tok = item - chunk_all * tokens;
-  const int b = (int)(tok / p.rows), i = (int)(tok - (long long)b * p.rows);
+  const int b = (int)(tok / (unsigned)p.rows), i = (int)(tok - (unsigned)b * p.rows);
 
   int n = p.map ? __ldg(p.map + i) : i;
   if (n >= p.N || n < -1) {
@@ -198,8 +196,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 #pragma unroll
   for (int u = 0; u < kRowsInFlight; ++u)
     if (h0 + u < h1) v[u] = load_row<D, HALVES>(x + (h0 + u) * x_step, ch);
-  const bool turn = p.cos != nullptr;
-  if (turn) load_angles<D>(p, b, n, ch, c, s);
+  if constexpr (TURN) load_angles<D>(p, b, n, ch, c, s);
   load_weights<D, HALVES>(p.w[which], ch, wa, wb);
 
   for (int h = h0; h < h1; h += kRowsInFlight) {
@@ -222,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       for (int e = 0; e < 4; ++e) {
         a[e] *= r * wa[e];
         bb[e] *= r * wb[e];
-        if (turn) {
+        if constexpr (TURN) {
           const float t = a[e] * c[e] - bb[e] * s[e];
           bb[e] = a[e] * s[e] + bb[e] * c[e];
           a[e] = t;
@@ -233,12 +230,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   }
 }
 
-// Backward.  The CTAs are split between q and k (ctas_q of them first); each
-// walks over its (token tile, head group) items with a fixed stride, keeps dw
-// in registers and writes one partial row, so the sums run in an order that
-// only the sizes and the grid fix.
-template <int D, typename T, bool HALVES>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRope p, int ctas_q) {
+// Backward.  The CTAs are split between q and k (ctas_q of them first) and
+// among their head groups; each walks over its token tiles with a fixed
+// stride, keeps dw in registers and writes one partial row, so the sums run in
+// an order that only the sizes and the grid fix.
+template <int D, typename T, bool HALVES, bool TURN>
+__global__ void __launch_bounds__(kThreads, kBwdPerSM) norm_rope_bwd_kernel(const __grid_constant__ NormRope p, int ctas_q) {
   constexpr int L = D / 8;
   constexpr int G = kThreads / L;               // lane groups
   __shared__ float red[G][D];
@@ -246,18 +243,14 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
   const unsigned mask = (L == 32 ? ~0u : ((1u << L) - 1)) << ((threadIdx.x % 32) / L * L);
   const int which = (int)blockIdx.x >= ctas_q;
   const int cta = which ? (int)blockIdx.x - ctas_q : (int)blockIdx.x;
-  const int ctas = which ? (int)gridDim.x - ctas_q : ctas_q;
-  const long long tokens = (long long)p.B * p.N;
-  const long long items = tokens * p.chunks[which];
+  const int ctas = (which ? (int)gridDim.x - ctas_q : ctas_q) / p.chunks[which];      // of one head group
+  const int h0 = cta / ctas * p.hb, h1 = min(h0 + p.hb, p.heads[which]);
+  const unsigned tokens = (unsigned)(p.B * p.N);
   float wa[4], wb[4], da[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
   load_weights<D, HALVES>(p.w[which], ch, wa, wb);
-  const bool turn = p.cos != nullptr;
 
-  for (long long item = (long long)cta * G + grp; item < items; item += (long long)ctas * G) {
-    const int chunk = (int)(item / tokens);
-    const long long tok = item - chunk * tokens;
-    const int b = (int)(tok / p.N), n = (int)(tok - (long long)b * p.N);
-    const int h0 = chunk * p.hb, h1 = min(h0 + p.hb, p.heads[which]);
+  for (unsigned tok = (unsigned)(cta % ctas) * G + grp; tok < tokens; tok += (unsigned)ctas * G) {
+    const int b = (int)(tok / (unsigned)p.N), n = (int)(tok - (unsigned)b * p.N);
     int i = p.map ? __ldg(p.map + n) : n;
     if (i >= p.rows || i < -1) {
       atomicOr(&g_rope_flags, kFlagIndex);
@@ -284,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
           v[u] = load_row<D, HALVES>(x + (h + u) * x_step, ch);
           gv[u] = load_row<D, HALVES>(dy + (h + u) * dy_step, ch);
         }
-      if (turn && !have) {
+      if (TURN && !have) {
         load_angles<D>(p, b, n, ch, c, s);
         have = true;
       }
@@ -297,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (turn) {
+          if constexpr (TURN) {
             const float t = ga[e] * c[e] + gb[e] * s[e];
             gb[e] = gb[e] * c[e] - ga[e] * s[e];
             ga[e] = t;
@@ -391,24 +384,30 @@ NormRope fill(const NormRopeArgs& a) {
   return p;
 }
 
-// Heads per lane group: as many as leave every SM some lane groups (the tables
-// are then read once for up to eight rows), one where the call is small and
-// its time is one row's latency.
+
+// Heads per lane group: a token's tables and indices are then read once for
+// that many rows.  One where the call is small and its time is one row's
+// latency, else up to 16, in equal groups of whole loads.
 int pick_hb(const NormRopeArgs& a, long long tokens, int d) {
   const long long groups = (long long)kNumSMs * (kThreads / (d / 8)) * 4;
-  int hb = 8;
+  const int most = std::max(a.heads[0], a.heads[1]);
+  int hb = 16;
   while (hb > 1 && tokens * ((a.heads[0] + hb - 1) / hb + (a.heads[1] + hb - 1) / hb) < groups) hb >>= 1;
-  return hb;
+  if (hb < kRowsInFlight) return hb;
+  const int parts = (most + hb - 1) / hb, each = (most + parts - 1) / parts;
+  return std::min(hb, (each + kRowsInFlight - 1) / kRowsInFlight * kRowsInFlight);
 }
 
 template <typename F>
-void by_type(int d, int f16, int halves, F&& f) {
+void by_type(int d, int f16, int halves, bool turn, F&& f) {
   auto t = [&](auto D_) {
     auto u = [&](auto z) {
-      using T = decltype(z);
-      if (halves) f(D_, z, std::true_type{});
-      else f(D_, z, std::false_type{});
-      (void)sizeof(T);
+      auto v = [&](auto H_) {
+        if (turn) f(D_, z, H_, std::true_type{});
+        else f(D_, z, H_, std::false_type{});
+      };
+      if (halves) v(std::true_type{});
+      else v(std::false_type{});
     };
     if (f16) u(__half{});
     else u(__nv_bfloat16{});
@@ -417,17 +416,16 @@ void by_type(int d, int f16, int halves, F&& f) {
   else t(std::integral_constant<int, 64>{});
 }
 
-// CTAs of q and k in the backward: about four per SM in all, in proportion to
-// the heads, none beyond the work.
+// CTAs of q and k in the backward: as many as are resident, in proportion to
+// the heads, the same number for each head group, none beyond the work.
 void bwd_ctas(const NormRopeArgs& a, int d, int hb, int* cq, int* ck) {
   const int G = kThreads / (d / 8);
-  const long long tokens = (long long)a.B * a.N;
-  const int total = kNumSMs * 4, heads = a.heads[0] + a.heads[1];
+  const long long tiles = ((long long)a.B * a.N + G - 1) / G;
+  const int total = kNumSMs * kBwdPerSM, heads = a.heads[0] + a.heads[1];
   for (int w = 0; w < 2; ++w) {
-    int* c = w ? ck : cq;
-    const long long tiles = (tokens * ((a.heads[w] + hb - 1) / hb) + G - 1) / G;
-    const long long share = a.heads[w] ? std::max(1, (int)((long long)total * a.heads[w] / heads)) : 0;
-    *c = (int)std::min(tiles, share);
+    const int chunks = (a.heads[w] + hb - 1) / hb;
+    const long long share = chunks ? std::max(1LL, (long long)total * a.heads[w] / heads / chunks) : 0;
+    *(w ? ck : cq) = (int)(chunks * std::min(tiles, share));
   }
 }
 
@@ -438,11 +436,10 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, int f16, cudaStream_t
   const long long tokens = (long long)a.B * a.rows;
   p.hb = pick_hb(a, tokens, d);
   for (int w = 0; w < 2; ++w) p.chunks[w] = (a.heads[w] + p.hb - 1) / p.hb;
-  const long long items = tokens * (p.chunks[0] + p.chunks[1]);
   const int G = kThreads / (d / 8);
-  const unsigned grid = (unsigned)((items + G - 1) / G);
-  by_type(d, f16, a.halves, [&](auto D_, auto z, auto H_) {
-    norm_rope_kernel<decltype(D_)::value, decltype(z), decltype(H_)::value><<<grid, kThreads, 0, st>>>(p);
+  const dim3 grid((unsigned)((tokens + G - 1) / G), (unsigned)(p.chunks[0] + p.chunks[1]));
+  by_type(d, f16, a.halves, a.cos != nullptr, [&](auto D_, auto z, auto H_, auto R_) {
+    norm_rope_kernel<decltype(D_)::value, decltype(z), decltype(H_)::value, decltype(R_)::value><<<grid, kThreads, 0, st>>>(p);
   });
   return cudaGetLastError();
 }
@@ -459,8 +456,9 @@ cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, int d, int f16, float* d
   for (int w = 0; w < 2; ++w) p.chunks[w] = (a.heads[w] + p.hb - 1) / p.hb;
   int cq = 0, ck = 0;
   bwd_ctas(a, d, p.hb, &cq, &ck);
-  by_type(d, f16, a.halves, [&](auto D_, auto z, auto H_) {
-    norm_rope_bwd_kernel<decltype(D_)::value, decltype(z), decltype(H_)::value><<<cq + ck, kThreads, 0, st>>>(p, cq);
+  by_type(d, f16, a.halves, a.cos != nullptr, [&](auto D_, auto z, auto H_, auto R_) {
+    norm_rope_bwd_kernel<decltype(D_)::value, decltype(z), decltype(H_)::value, decltype(R_)::value>
+        <<<cq + ck, kThreads, 0, st>>>(p, cq);
   });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (dwq == nullptr && dwk == nullptr)) return e;

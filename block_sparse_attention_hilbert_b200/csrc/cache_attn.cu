@@ -285,8 +285,24 @@ struct Window {
   float ks, vs;
 };
 
+// With lists, the entry of this lane and the one before it are read ahead of
+// what bounds them (`j0 + lane * WARPS < j1` and j1 within the list's capacity).
+struct Entry {
+  int j, before;
+};
 template <int WARPS>
-__device__ __forceinline__ Window load_window(const AttnArgs& p, const Segment& s, int first, int len) {
+__device__ __forceinline__ Entry load_entry(const AttnArgs& p, const Segment& s, int first, int j1) {
+  Entry e{first + (int)(threadIdx.x % 32) * WARPS, -1};
+  if (p.idx && e.j < j1) {
+    const int32_t* list = p.idx + (((long long)s.b * p.Tq + s.t) * p.c.heads + s.h) * p.cap + e.j;
+    e.before = e.j > 0 ? __ldg(list - 1) : -1;
+    e.j = __ldg(list);
+  }
+  return e;
+}
+
+template <int WARPS>
+__device__ __forceinline__ Window load_window(const AttnArgs& p, const Segment& s, int first, int len, Entry e) {
   Window w;
   const int lane = threadIdx.x % 32;
   const int left = s.j1 - first;
@@ -295,20 +311,14 @@ __device__ __forceinline__ Window load_window(const AttnArgs& p, const Segment& 
   w.tok = 1 << 30;
   w.ks = w.vs = 0.f;
   if (lane < w.n) {
-    int j = first + lane * WARPS;
-    bool ok = p.idx || len > 0;              // an empty sequence has one unit, and nothing in it
-    if (p.idx) {
-      const int32_t* list = p.idx + (((long long)s.b * p.Tq + s.t) * p.c.heads + s.h) * p.cap;
-      const int before = j > 0 ? __ldg(list + j - 1) : -1;
-      j = __ldg(list + j);
-      ok = j > before && j >= 0 && j < p.c.max_blocks && (long long)j * kBlock < len;
-    }
-    const int page = ok ? __ldg(p.c.table + (long long)s.b * p.c.max_blocks + j) : -1;
+    // (an empty sequence has one unit, and nothing in it)
+    bool ok = p.idx ? e.j > e.before && e.j >= 0 && e.j < p.c.max_blocks && (long long)e.j * kBlock < len : len > 0;
+    const int page = ok ? __ldg(p.c.table + (long long)s.b * p.c.max_blocks + e.j) : -1;
     ok = ok && (unsigned)page < (unsigned)p.c.n_pages;
     if (ok) {
       const long long cell = (long long)page * p.c.heads + s.h;
       w.row = (int)(cell * kBlock);
-      w.tok = j * kBlock;
+      w.tok = e.j * kBlock;
       w.ks = __ldg(p.c.k_scale + cell);
       w.vs = __ldg(p.c.v_scale + cell);
     } else if (p.idx || len > 0) {
@@ -365,6 +375,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   constexpr int SUMS = RING * TILE / 4;      // floats between two warps' rings
   const uint32_t ring = ring0 + warp * (RING * TILE);
   const uint32_t bar = tc::su32(bars) + warp * (RING * 8);
+  cudaTriggerProgrammaticLaunchCompletion();  // the joining kernel may take its places; it waits for this one's end
   const Shares sh = shares_of(p);
   if ((int)blockIdx.x >= sh.ctas) return;
   if (threadIdx.x == 0) {
@@ -404,11 +415,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       before = u;
       seq += 1;
     }
+    if (p.whole && p.idx) s.j1 = p.cap;
+    const Entry ahead = load_entry<kWarps>(p, s, s.j0 + warp, s.j1);
+    int n = p.idx ? __ldg(p.cnt + ((long long)s.b * p.Tq + s.t) * p.c.heads + s.h) : 0;
     const int len = seq_len(p, s.b);
-    if (p.whole) s.j1 = p.idx ? p.cap : blocks_of(len);
+    if (p.whole && !p.idx) s.j1 = blocks_of(len);
     if (p.idx) {
-      const long long r = ((long long)s.b * p.Tq + s.t) * p.c.heads + s.h;
-      int n = __ldg(p.cnt + r);
       if (n < 0 || n > p.cap) {
         if (threadIdx.x == 0) atomicOr(&g_cattn_flags, kFlagIndex);
         n = min(max(n, 0), p.cap);
@@ -418,11 +430,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
     // windows of blocks: `cur` is consumed while loads may run into `nxt`
     int at = s.j0 + warp;
-    Window cur = load_window<kWarps>(p, s, at, len);
+    Window cur = load_window<kWarps>(p, s, at, len, ahead);
     at += 32 * kWarps;
     Window nxt;
     nxt.n = 0;
-    if (at < s.j1) nxt = load_window<kWarps>(p, s, at, len);
+    if (at < s.j1) nxt = load_window<kWarps>(p, s, at, len, load_entry<kWarps>(p, s, at, s.j1));
     at += 32 * kWarps;
     uint32_t fetched = 0;                     // tiles of `cur` (and on into `nxt`) asked for: K then V of each block
     auto fetch = [&]() {                      // one more tile, if there is one
@@ -632,7 +644,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       fetched -= 2u * (uint32_t)cur.n;
       cur = nxt;
       nxt.n = 0;
-      if (at < s.j1) nxt = load_window<kWarps>(p, s, at, len);
+      if (at < s.j1) nxt = load_window<kWarps>(p, s, at, len, load_entry<kWarps>(p, s, at, s.j1));
       at += 32 * kWarps;
     }
 
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
   constexpr int ROWS = 8 * NR;
   __shared__ float4 sums[G][V];
   __shared__ float rowsum[G];
-  cudaGridDependencySynchronize();
+  // (everything up to the wait reads only what was there before the first kernel)
   const Shares sh = shares_of(p);
   const int cta = blockIdx.x, row = blockIdx.y;
   if (cta + 1 >= sh.ctas) return;
@@ -729,6 +741,7 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
   int t, hg;
   if (!row_of<ROWS>(p, s, row, &t, &hg)) return;
 
+  cudaGridDependencySynchronize();
   const float* stats = p.part + 2LL * p.grid * ROWS * D;
   auto slot_of = [&](int c) { return (2LL * c + (c == cta ? 1 : 0)) * ROWS + row; };
   float top = -INFINITY;

@@ -593,8 +593,9 @@ cudaError_t launch_cache_select(const CacheArgs& c, const void* q, int heads_q, 
   cfg.numAttrs = 1;
   cudaError_t e = cudaSuccess;
   by_d_type(c.d, f16, [&](auto D_, auto z) {
-    auto kernel = cache_select_kernel<decltype(D_)::value, decltype(z)>;
-    if (smem > 32768) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr auto kernel = cache_select_kernel<decltype(D_)::value, decltype(z)>;
+    // (the most that a call can ask for: the keys of 32768 blocks, 128 heads)
+    if (smem > 32768) e = allow_smem<kernel>(32768 * 4 + 128 * 132 + 16);
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
   });
   return e;

@@ -794,9 +794,9 @@ bool map_codes(CUtensorMap* m, const void* base, long long rows, int d) {
 
 template <int D, typename T, bool I8, int NR>
 cudaError_t run(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& p, cudaStream_t st) {
-  auto kernel = cache_attn_kernel<D, T, I8, NR>;
+  constexpr auto kernel = cache_attn_kernel<D, T, I8, NR>;
   constexpr int smem = Cta<D, NR>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem<kernel>(smem);
   if (e != cudaSuccess) return e;
   kernel<<<p.grid, Cta<D, NR>::kThreads, smem, st>>>(mk, mv, p);
   e = cudaGetLastError();

@@ -69,7 +69,7 @@ class Schedule(ctypes.Structure):
                 ("end", ctypes.c_float), ("refresh_every", ctypes.c_int32)]
 
 
-class NormRope(ctypes.Structure):
+class NormRopeParams(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("rows", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("pairing", ctypes.c_int32), ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * 3),
@@ -151,9 +151,9 @@ _SIGS = {
                                           ctypes.POINTER(MaskParams), ctypes.POINTER(ctypes.c_int32)]),
     "svsa_anchor_offset": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                           ctypes.POINTER(ctypes.c_int32)]),
-    "svsa_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.POINTER(NormRope), ctypes.c_void_p]),
-    "svsa_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(NormRope)]),
-    "svsa_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.c_void_p] * 14 + [ctypes.POINTER(NormRope), ctypes.c_void_p,
+    "svsa_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.POINTER(NormRopeParams), ctypes.c_void_p]),
+    "svsa_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(NormRopeParams)]),
+    "svsa_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.c_void_p] * 14 + [ctypes.POINTER(NormRopeParams), ctypes.c_void_p,
                                                                       ctypes.c_size_t, ctypes.c_void_p]),
     "svsa_cache_append": (ctypes.c_int, [ctypes.POINTER(Cache)] + [ctypes.c_void_p] * 4 +
                           [ctypes.POINTER(CacheTokens), ctypes.c_void_p]),
@@ -392,31 +392,31 @@ def _native():
         spec = importlib.util.spec_from_file_location("_svsa_binding", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-        m.init(NormRope, Cache, CacheTokens, CacheQuery)
+        m.init(NormRopeParams, Cache, CacheTokens, CacheQuery)
         _native_module = m
     return _native_module
 
 
 def norm_rope_params(q, k, cos=None, pos=None, *, rows: int | None = None, pairs=(), halves: bool = False,
-                     eps: float = 1e-6) -> NormRope:
+                     eps: float = 1e-6) -> NormRopeParams:
     """Parameters of svsa_qk_norm_rope for q [B, heads_q, N, d] and k [B, heads_k, N, d] or None (views with a
     contiguous last dimension).  pairs: pairs of each position axis; pos int32 [B or 1, N, axes]; cos fp32
     [table_rows, d / 2].  rows: rows of the outputs (N without a token map)."""
     return (_native_module or _native()).norm_rope_params(q, k, cos, pos, rows, pairs, halves, eps)
 
 
-def svsa_qk_norm_rope(q, k, wq, wk, cos, sin, pos, perm, yq, yk, p: NormRope, stream=None) -> None:
+def svsa_qk_norm_rope(q, k, wq, wk, cos, sin, pos, perm, yq, yk, p: NormRopeParams, stream=None) -> None:
     """Norm, rotation and token order of q and k (k, wk, yk None without keys; perm None for raster order)."""
     status = (_native_module or _native()).qk_norm_rope(q, k, wq, wk, cos, sin, pos, perm, yq, yk, p, stream)
     if status:
         _check(status, "svsa_qk_norm_rope")
 
 
-def svsa_qk_norm_rope_bwd_workspace_bytes(p: NormRope) -> int:
+def svsa_qk_norm_rope_bwd_workspace_bytes(p: NormRopeParams) -> int:
     return (_native_module or _native()).qk_norm_rope_bwd_workspace_bytes(p)
 
 
-def svsa_qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, cos, sin, pos, iperm, dq, dk, dwq, dwk, p: NormRope, ws,
+def svsa_qk_norm_rope_bwd(dyq, dyk, q, k, wq, wk, cos, sin, pos, iperm, dq, dk, dwq, dwk, p: NormRopeParams, ws,
                           ws_bytes: int, stream=None) -> None:
     """Gradients of svsa_qk_norm_rope: dq, dk in q's and k's shapes, with strides of their own; dwq, dwk fp32 [d] (or
     None).  iperm: the output row of each token (None for raster order)."""
@@ -474,4 +474,5 @@ def svsa_sync_status(stream=None) -> None:
     _check(lib().svsa_sync_status(_stream(stream)), "svsa_sync_status")
 
 
+from .stream import BlockCache, NormRope, grid_positions, rope_tables  # noqa: E402,F401
 from .pipeline import CapturedLayer, SparseVideoAttention, LayerBuffers  # noqa: E402,F401

@@ -122,7 +122,7 @@ class Struct {
   Py_buffer buf_;
 };
 
-PyObject* g_types[4];                            // NormRope, Cache, CacheTokens, CacheQuery
+PyObject* g_types[4];                            // NormRopeParams, Cache, CacheTokens, CacheQuery
 PyObject* g_device;                              // "device"
 
 // A new structure of g_types[which] holding `value`.
@@ -455,7 +455,7 @@ PyObject* rope_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// init(NormRope, Cache, CacheTokens, CacheQuery): the package's ctypes structures
+// init(NormRopeParams, Cache, CacheTokens, CacheQuery): the package's ctypes structures
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() {
     count(n, 4);

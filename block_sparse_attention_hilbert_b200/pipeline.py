@@ -104,7 +104,8 @@ class SparseVideoAttention:
     def __init__(self, B, heads, T, H, W, d, *, order="hilbert", select="threshold", tau=0.9,
                  keep_frac=0.25, sub_block=64, win_t=2, win_rows=1, n_anchors=0, routing=False,
                  compensate=False, keep_bits=False, schedule=None, cluster_rounds=3, attn_passes=None,
-                 seed=0, scorer="pooled", check_mask=False, pair_blocks=False, paired_split=False, device="cuda"):
+                 seed=0, scorer="pooled", check_mask=False, pair_blocks=False, paired_split=False, device="cuda",
+                 norm_rope=None):
         """order: "raster", "hilbert" or "cocluster" (a per-head semantic order from
         bidirectional query-key co-clustering, built from the first inputs and
         kept until `rebuild_order()`).  schedule: optional (n_steps, dense_steps,
@@ -124,7 +125,11 @@ class SparseVideoAttention:
         kept-block bitmap).  pair_blocks: let svsa_build_mask pair the query
         blocks by kept-list overlap for that split (else blocks 2p and 2p + 1
         go together).  Both are off by default: on B200 the 64-row kernel
-        alone is the faster one on the sparse masks measured."""
+        alone is the faster one on the sparse masks measured.  norm_rope: a
+        NormRope layer with the positions of the grid's tokens, (layer, pos)
+        or (layer, None) for one without rotation: q and k are normed and
+        rotated in the pass that reorders them (device calls; not with the
+        co-clustering order, whose maps differ per head)."""
         self.B, self.heads, self.T, self.H, self.W, self.d = B, heads, T, H, W, d
         self.N = T * H * W
         self.nb = -(-self.N // BLOCK)
@@ -132,6 +137,9 @@ class SparseVideoAttention:
         self.cocluster = order == "cocluster"
         self.cluster_rounds = int(cluster_rounds)
         self.order = ORDER_RASTER if self.cocluster else _ORDERS[order]
+        if norm_rope is not None and self.cocluster:
+            raise ValueError("norm_rope needs one token order for all heads (raster or hilbert)")
+        self.norm_rope = norm_rope
         if self.cocluster and select == "structured":
             raise ValueError("the structured rule needs a geometric order (raster or hilbert)")
         self.select = _SELECTS[select]
@@ -194,8 +202,14 @@ class SparseVideoAttention:
             svsa_reorder_heads(k, b.kp, b.perm_k, self.shape, stream)
             svsa_reorder_values_heads(v, b.vp, b.perm_k, self.shape, stream)
             return
-        svsa_reorder(q, b.qp, b.perm, self.shape, stream)
-        svsa_reorder(k, b.kp, b.perm, self.shape, stream)
+        if self.norm_rope is not None:
+            layer, pos = self.norm_rope
+            if not v.is_contiguous():
+                raise ValueError("v must be contiguous [B, heads, N, d] (q and k may be views)")
+            layer(q, k, pos, perm=b.perm, out=(b.qp, b.kp), stream=stream)
+        else:
+            svsa_reorder(q, b.qp, b.perm, self.shape, stream)
+            svsa_reorder(k, b.kp, b.perm, self.shape, stream)
         svsa_reorder_values(v, b.vp, b.perm, self.shape, stream)
 
     def build_mask(self, step: int = 0, stream=None):
@@ -237,7 +251,7 @@ class SparseVideoAttention:
         p, rebuild = svsa_schedule_step(self.schedule, step, base)
         self.params = p
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)      # (q may be a view with norm_rope)
         build = rebuild or not self.mask_ready
         self.reorder(q, k, v, stream)
         if build:
@@ -268,6 +282,8 @@ class SparseVideoAttention:
         run on the current stream once its event has fired, and its output is
         copied out on a third stream.  The current stream waits for the last
         copy, so synchronising it covers the layer."""
+        if self.norm_rope is not None:
+            raise ValueError("forward_host reorders its rows in groups and has no norm_rope; use a device call")
         b = self.buf
         rows = self.B * self.heads
         if getattr(self, "_stage", None) is None:
@@ -370,7 +386,7 @@ class SparseVideoAttention:
 
     def __call__(self, q, k, v, *, out=None, step: int = 0, reuse_mask: bool = False, stream=None):
         if out is None:
-            out = torch.empty_like(q)
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)      # (q may be a view with norm_rope)
         self.reorder(q, k, v, stream)
         if not (reuse_mask and self.mask_ready):
             self.build_mask(step, stream)

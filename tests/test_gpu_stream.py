@@ -725,3 +725,72 @@ def test_list_entries_that_are_not_ascending_or_past_the_end_are_left_out_and_re
         lists = np.empty((1, 1, 1), dtype=object)
         lists[0, 0, 0] = kept
         _check_attention(gpu, q, o, lse, True, lists)
+
+
+# ---- the layer classes ------------------------------------------------------------------------------
+
+def test_layer_classes_run_a_stream_and_its_gradients():
+    """NormRope and BlockCache against the oracle over a few pieces, and NormRope.backward against autograd of the same
+    formula in 64 bits."""
+    B, h, d, T, H, W = 1, 2, 64, 1, 6, 9
+    N = T * H * W
+    rope = svsa.NormRope(d, pairs=(12, 10, 10), rows=20, halves=True, wq=torch.linspace(0.5, 1.5, d).cuda(), wk=None)
+    cache = svsa.BlockCache(B, h, d, 4 * N, code="i8")
+    ref = stream.BlockCache(*(t.cpu().numpy() for t in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale,
+                                                        cache.v_scale, cache.mean, cache.mean_scale, cache.table,
+                                                        cache.length)), "i8")
+    for f in range(4):
+        x = torch.randn(B, N, 3 * h, d, generator=_gen(30 + f)).to(BF).cuda()
+        q, k, v = (x[:, :, i * h:(i + 1) * h].transpose(1, 2) for i in range(3))
+        pos = svsa.grid_positions(T, H, W, frame=f)
+        yq, yk = rope(q, k, pos)
+        cache.append(yk, v)
+        ref.append(_np(yk), _np(v), [N])
+        assert np.count_nonzero(cache.k.view(torch.uint8).cpu().numpy() != ref.k) == 0
+        idx, cnt = cache.select(yq, 2, causal=False)
+        o = cache.attend(yq, idx, cnt, causal=False)
+        want, _ = stream.cache_attention(ref, _np(yq), False, _lists(idx, cnt))
+        assert np.abs(_np(o) - want).max() <= (2.0**-11 + 2.0**-12 + 2.0**-8) * np.abs(ref.tokens(0, 0)[1]).max() * 2
+    svsa.svsa_sync_status()
+    # gradients
+    gq, gk = (torch.randn(B, h, N, d, generator=_gen(i)).to(BF).cuda() for i in (1, 2))
+    dq, dk, dwq, dwk = rope.backward(gq, gk, q, k, pos)
+    axis = torch.repeat_interleave(torch.arange(3), torch.tensor(rope.pairs)).cuda()
+    ang = [t.double()[pos[0].long()[:, axis], torch.arange(d // 2, device="cuda")] for t in (rope.cos, rope.sin)]
+    for x, w, g, got, gw in ((q, rope.wq, gq, dq, dwq), (k, torch.ones(d).cuda(), gk, dk, dwk)):
+        a, b = x.double().requires_grad_(), w.double().requires_grad_()
+        y = a / (a.square().mean(-1, keepdim=True) + rope.eps).sqrt() * b
+        lo, hi = y[..., :d // 2], y[..., d // 2:]
+        y = torch.cat([lo * ang[0] - hi * ang[1], lo * ang[1] + hi * ang[0]], -1)
+        ga, gb = torch.autograd.grad(y, (a, b), g.double())
+        assert float((got.double() - ga).abs().max()) <= 2.0**-8 * float(ga.abs().max())
+        # (B h N = 108 rows, fp32 sums of terms of unit size: (108 + 64) 2^-24 of their total)
+        terms = (g.double().abs().amax(-1, keepdim=True) * (a / a.square().mean(-1, keepdim=True).sqrt()).abs()).sum((0, 1, 2))
+        assert torch.all((gw.double() - gb).abs() <= 172 * 2.0**-24 * 2 * terms)
+    cache.reset()
+    assert torch.all(cache.attend(yq) == 0)
+
+
+@pytest.mark.parametrize("order", ["raster", "hilbert"])
+def test_sparse_layer_with_norm_and_rotation(order):
+    """SparseVideoAttention with norm_rope gives, bit for bit, the layer on queries and keys normed and rotated
+    beforehand."""
+    B, h, T, H, W, d = 1, 2, 3, 8, 10, 128
+    N = T * H * W
+    x = torch.randn(B, N, 3 * h, d, generator=_gen(40)).to(BF).cuda()
+    q, k, v = (x[:, :, i * h:(i + 1) * h].transpose(1, 2) for i in range(3))
+    v = v.contiguous()
+    rope = svsa.NormRope(d, pairs=(24, 20, 20), rows=16, wq=torch.linspace(0.8, 1.2, d).cuda())
+    pos = svsa.grid_positions(T, H, W)
+    kw = dict(order=order, select="topk", keep_frac=0.5)
+    got = svsa.SparseVideoAttention(B, h, T, H, W, d, norm_rope=(rope, pos), **kw)
+    o = got(q, k, v)
+    assert o.is_contiguous()
+    yq, yk = rope(q, k, pos)
+    want = svsa.SparseVideoAttention(B, h, T, H, W, d, **kw)(yq, yk, v)
+    svsa.svsa_sync_status()
+    assert torch.equal(o, want)
+    with pytest.raises(ValueError):
+        got.forward_host(q, k, v, o)
+    with pytest.raises(ValueError):
+        got(q, k, x[:, :, 2 * h:].transpose(1, 2))         # a view as v

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_sparse_attention_hilbert_b200 as svsa
-from block_sparse_attention_hilbert_b200 import Cache, CacheQuery, CacheTokens, NormRope
+from block_sparse_attention_hilbert_b200 import Cache, CacheQuery, CacheTokens, NormRopeParams
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -20,7 +20,7 @@ def test_struct_layouts_match_the_c_compiler(tmp_path):
     import subprocess
     if shutil.which("gcc") is None:
         pytest.skip("gcc not available")
-    structs = {"svsa_norm_rope": NormRope, "svsa_cache": Cache, "svsa_cache_tokens": CacheTokens,
+    structs = {"svsa_norm_rope": NormRopeParams, "svsa_cache": Cache, "svsa_cache_tokens": CacheTokens,
                "svsa_cache_query": CacheQuery}
     lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "svsa.h"', "int main(void) {"]
     for cname, cls in structs.items():
@@ -51,7 +51,7 @@ def _rope(**kw):
              table_rows=16, eps=1e-6, pos_stride=0, q_stride=(4 * 640, 640, 64), k_stride=(2 * 640, 640, 64),
              dq_stride=(4 * 640, 640, 64), dk_stride=(2 * 640, 640, 64))
     f.update(kw)
-    return NormRope(*(f[n] for n, _ in NormRope._fields_))
+    return NormRopeParams(*(f[n] for n, _ in NormRopeParams._fields_))
 
 
 def _fwd(p, q=16, k=32, wq=48, wk=64, cos=80, sin=96, pos=112, mp=None, yq=144, yk=160):
@@ -215,3 +215,30 @@ def test_binding_checks_tensors():
         svsa.svsa_cache_attn(c, q, None, None, torch.empty_like(q).half(), None, qp, None, 0)
     with pytest.raises(ValueError):
         svsa.svsa_cache_select(c, q, torch.zeros(2, 3, 2, 3, dtype=torch.int32), torch.zeros(2, 3, 2, dtype=torch.int32), qp)
+
+
+def test_layer_classes_check_their_arguments():
+    with pytest.raises(ValueError):
+        svsa.NormRope(64, pairs=(16, 8), rows=4, device="cpu")
+    with pytest.raises(ValueError):
+        svsa.NormRope(64, pairs=(32,), device="cpu")
+    with pytest.raises(ValueError):
+        svsa.BlockCache(2, 1, 64, 200, n_pages=7, device="cpu")
+    with pytest.raises(ValueError):
+        svsa.BlockCache(2, 1, 64, 200, table=torch.zeros(2, 4, dtype=torch.int32), device="cpu")
+    c = svsa.BlockCache(2, 1, 64, 200, code="i8", means=False, device="cpu")
+    assert c.table.tolist() == [[0, 1, 2, 3], [4, 5, 6, 7]] and c.cache.mean is None and c.cache.code == svsa.CODE_I8
+    with pytest.raises(ValueError):
+        svsa.SparseVideoAttention(1, 1, 2, 8, 8, 64, order="cocluster", norm_rope=(None, None), device="cpu")
+
+
+def test_rope_tables_and_grid_positions():
+    cos, sin = svsa.rope_tables(9, (3, 1), theta=100.0, device="cpu")
+    assert cos.shape == (9, 4)
+    f = torch.tensor([1.0, 100.0 ** (-1 / 3), 100.0 ** (-2 / 3), 1.0], dtype=torch.float64)
+    want = torch.arange(9, dtype=torch.float64)[:, None] * f
+    # one rounding to fp32: at most half a step
+    assert (cos.double() - want.cos()).abs().max() <= 2.0**-24 and (sin.double() - want.sin()).abs().max() <= 2.0**-24
+    pos = svsa.grid_positions(2, 3, 4, frame=5, device="cpu")
+    assert pos.shape == (1, 24, 3) and pos[0, 0].tolist() == [5, 0, 0] and pos[0, 23].tolist() == [6, 2, 3]
+    assert pos[0, 1 * 12 + 2 * 4 + 1].tolist() == [6, 2, 1]

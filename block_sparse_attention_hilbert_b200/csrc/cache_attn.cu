@@ -46,6 +46,7 @@ static __device__ unsigned int g_cattn_flags;
 namespace {
 
 constexpr float kShift = 14.f;              // weights are held times 2^kShift
+constexpr int kMaxSmallRows = 32;           // rows per key head up to which 16-row tiles are used
 constexpr int kMinUnits = 8;                // blocks of a CTA at least, where there are as many
 
 struct AttnArgs {
@@ -714,18 +715,20 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   }
 }
 
-// Joins the items that several CTAs shared: block (c, row) looks at the item
-// that the start of CTA c + 1's share splits, if c holds its first unit.
-template <int D, typename T, int NR>
+#include "cache_attn_rows.cuh"
+
+// Joins the items that several CTAs shared: block (c, y) looks at the item
+// that the start of CTA c + 1's share splits, and if c holds its first unit
+// joins its rows y, y + gridDim.y, ...
+template <int D, typename T, int ROWS>
 __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_constant__ AttnArgs p) {
   constexpr int V = D / 4;                      // lanes of four columns
   constexpr int G = 128 / V;
-  constexpr int ROWS = 8 * NR;
   __shared__ float4 sums[G][V];
   __shared__ float rowsum[G];
   // (everything up to the wait reads only what was there before the first kernel)
   const Shares sh = shares_of(p);
-  const int cta = blockIdx.x, row = blockIdx.y;
+  const int cta = blockIdx.x;
   if (cta + 1 >= sh.ctas) return;
   const unsigned u = sh.first(cta + 1);
   int seq = 0;
@@ -738,45 +741,49 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
   const unsigned u0 = u - s.j0;
   if (sh.of(u0) != cta) return;                 // an earlier CTA holds the item's first unit
   const int last = sh.of(u0 + units - 1);
-  int t, hg;
-  if (!row_of<ROWS>(p, s, row, &t, &hg)) return;
 
   cudaGridDependencySynchronize();
   const float* stats = p.part + 2LL * p.grid * ROWS * D;
-  auto slot_of = [&](int c) { return (2LL * c + (c == cta ? 1 : 0)) * ROWS + row; };
-  float top = -INFINITY;
-  for (int c = cta + (int)threadIdx.x % 32; c <= last; c += 32) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c)));
-  top = warp_max(top);
-  const float z = top == -INFINITY ? 0.f : top;
   const int v = threadIdx.x % V, g = threadIdx.x / V;
-  float sum = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int row = blockIdx.y; row < ROWS; row += gridDim.y) {
+    int t, hg;
+    if (!row_of<ROWS>(p, s, row, &t, &hg)) return;            // (rows past the end are the last ones)
+    auto slot_of = [&](int c) { return (2LL * c + (c == cta ? 1 : 0)) * ROWS + row; };
+    float top = -INFINITY;
+    for (int c = cta + (int)threadIdx.x % 32; c <= last; c += 32) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c)));
+    top = warp_max(top);
+    const float z = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = cta + g; c <= last; c += G) {
-    const long long k = slot_of(c);
-    const float w = tc::ex2(__ldcg(stats + 2 * k) - z);
-    sum += w * __ldcg(stats + 2 * k + 1);
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part + k * D) + v);
-    x.x += w * a.x;
-    x.y += w * a.y;
-    x.z += w * a.z;
-    x.w += w * a.w;
-  }
-  sums[g][v] = x;
-  if (v == 0) rowsum[g] = sum;
-  __syncthreads();
-  if (g != 0) return;
-  x = make_float4(0.f, 0.f, 0.f, 0.f);
-  sum = 0.f;
+    for (int c = cta + g; c <= last; c += G) {
+      const long long k = slot_of(c);
+      const float w = tc::ex2(__ldcg(stats + 2 * k) - z);
+      sum += w * __ldcg(stats + 2 * k + 1);
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part + k * D) + v);
+      x.x += w * a.x;
+      x.y += w * a.y;
+      x.z += w * a.z;
+      x.w += w * a.w;
+    }
+    sums[g][v] = x;
+    if (v == 0) rowsum[g] = sum;
+    __syncthreads();
+    if (g == 0) {
+      x = make_float4(0.f, 0.f, 0.f, 0.f);
+      sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    x.x += sums[i][v].x;
-    x.y += sums[i][v].y;
-    x.z += sums[i][v].z;
-    x.w += sums[i][v].w;
-    sum += rowsum[i];
+      for (int i = 0; i < G; ++i) {
+        x.x += sums[i][v].x;
+        x.y += sums[i][v].y;
+        x.z += sums[i][v].z;
+        x.w += sums[i][v].w;
+        sum += rowsum[i];
+      }
+      write_out<D, T>(p, s, t, hg, 4 * v, x, top, sum);
+    }
+    __syncthreads();
   }
-  write_out<D, T>(p, s, t, hg, 4 * v, x, top, sum);
 }
 
 // Byte view of the codes, [rows, d]: boxes of one block, swizzled over the row.
@@ -792,6 +799,20 @@ bool map_codes(CUtensorMap* m, const void* base, long long rows, int d) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int D, typename T, int ROWS>
+cudaError_t join(const AttnArgs& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.grid, ROWS < 16 ? ROWS : 16);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, T, ROWS>, p);
+}
+
 template <int D, typename T, bool I8, int NR>
 cudaError_t run(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& p, cudaStream_t st) {
   constexpr auto kernel = cache_attn_kernel<D, T, I8, NR>;
@@ -800,22 +821,30 @@ cudaError_t run(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& p,
   if (e != cudaSuccess) return e;
   kernel<<<p.grid, Cta<D, NR>::kThreads, smem, st>>>(mk, mv, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.whole) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.grid, 8 * NR);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, T, NR>, p);
+  return e != cudaSuccess || p.whole ? e : join<D, T, 8 * NR>(p, st);
 }
+
+template <int D, typename T, bool I8>
+cudaError_t run_rows(const AttnArgs& p, cudaStream_t st) {
+  constexpr auto kernel = cache_attn_rows_kernel<D, T, I8>;
+  cudaError_t e = allow_smem<kernel>(kRowsSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.grid, kRowsThreads, kRowsSmem, st>>>(p);
+  e = cudaGetLastError();
+  return e != cudaSuccess || p.whole ? e : join<D, T, kTileRows>(p, st);
+}
+
+// Rows of a tile for this many query rows per key head (whole cache) or per
+// list.  ROWS_NOTE
+int tile_rows(long long rows, bool lists) { return rows <= 8 ? 8 : rows <= kMaxSmallRows || lists ? 16 : kTileRows; }
 
 }  // namespace
 
-size_t cache_attn_workspace_bytes(int d) { return (size_t)kNumSMs * 2 * 16 * (d + 2) * sizeof(float); }
+size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq) {
+  // (with or without lists: the larger)
+  const int rows = tile_rows((long long)heads_q / c.heads * Tq, false);
+  return (size_t)kNumSMs * 2 * std::max(rows, 16) * (c.d + 2) * sizeof(float);
+}
 
 cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal,
                               const int32_t* idx, const int32_t* cnt, int cap, void* o, float* lse, void* ws,
@@ -834,8 +863,8 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   p.cap = cap;
   p.group = heads_q / c.heads;
   const long long rows = idx ? p.group : (long long)p.group * Tq;
-  const int nr = rows <= 8 ? 1 : 2;
-  p.tiles = ceil_div(rows, 8 * nr);
+  const int tile = tile_rows(rows, idx != nullptr);
+  p.tiles = ceil_div(rows, tile);
   p.grid = kNumSMs;
   // Whole items per CTA where no item is longer than two rounds of the warps,
   // or where the items, all alike, fill the CTAs to within 5%: the second
@@ -845,13 +874,16 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   p.whole = (idx ? cap : c.max_blocks) <= 16 || (idx && items * 20 >= rounds * kNumSMs * 19);
   CUtensorMap mk, mv;
   const long long map_rows = (long long)c.n_pages * c.heads * kBlock;
-  if (!map_codes(&mk, c.k, map_rows, c.d) || !map_codes(&mv, c.v, map_rows, c.d)) return cudaErrorInvalidValue;
+  if (tile <= 16 && (!map_codes(&mk, c.k, map_rows, c.d) || !map_codes(&mv, c.v, map_rows, c.d)))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   auto by_rows = [&](auto D_, auto z, auto i8) {
     constexpr int D = decltype(D_)::value;
     constexpr bool I8 = decltype(i8)::value;
     using T = decltype(z);
-    e = nr == 1 ? run<D, T, I8, 1>(mk, mv, p, st) : run<D, T, I8, 2>(mk, mv, p, st);
+    e = tile == 8    ? run<D, T, I8, 1>(mk, mv, p, st)
+        : tile == 16 ? run<D, T, I8, 2>(mk, mv, p, st)
+                     : run_rows<D, T, I8>(p, st);
   };
   auto by_code = [&](auto D_, auto z) {
     if (c.i8) by_rows(D_, z, std::true_type{});
@@ -870,8 +902,8 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
 // Units of one call at most (32-bit counters).
 long long cache_attn_units(const CacheArgs& c, int heads_q, int Tq, const int32_t* idx, int cap) {
   const long long group = heads_q / c.heads, rows = idx ? group : group * Tq;
-  const long long tiles = (rows + (rows <= 8 ? 7 : 15)) / (rows <= 8 ? 8 : 16);
-  return (long long)c.B * (idx ? Tq : 1) * c.heads * tiles * (idx ? cap : c.max_blocks);
+  const int tile = tile_rows(rows, idx != nullptr);
+  return (long long)c.B * (idx ? Tq : 1) * c.heads * ((rows + tile - 1) / tile) * (idx ? cap : c.max_blocks);
 }
 
 cudaError_t cattn_flags(unsigned int* v, cudaStream_t st) { return read_and_clear_flags(g_cattn_flags, v, st); }

@@ -1,0 +1,555 @@
+// Attention over the block cache for many query rows per key head (chunks of
+// a stream): tcgen05 tiles of 128 rows.  Part of cache_attn.cu, whose items,
+// shares and joining kernel it uses.
+//
+// With more than a few 16-row tiles the time is no longer that of reading the
+// codes but of widening them again for every tile and of mma.sync.  Here a
+// page is widened once per 128 rows, to fp16 in shared memory in the layout
+// that the MMA reads, and both products run on the 5th-generation tensor
+// cores, two pages to a step:
+//     S [128 x 128] = Q [128 x d] K^T       (fp16, the codes themselves)
+//     O_h [128 x d] += P_h [128 x 64] V_h   (h = 0, 1: the step's pages; P in tensor memory)
+// Roles: warp 0 issues the MMAs; warps 4-11 are two softmax warpgroups, one
+// thread per query row each, one for each page of a step, with a maximum, a
+// row sum and an accumulator of their own, merged at the item's end; warps
+// 1-3 widen the pages (loads two tiles ahead in registers).  (One page to a
+// step, with the same roles, left the issuing thread's waits the bound: 694 us
+// where this takes FRAME us, 1560 queries x 12 heads over 32,760 tokens.)
+//
+// Scales: the key scale joins the softmax's factor.  The value scale goes
+// into the weights as an exponent, P = 2^(y - m'), y = s + log2 vs, with a
+// reference m' of its own for y, so the fp16 weights are measured against the
+// largest contribution to the output whatever the scales; the row sum is
+// kept against the maximum of s.  (A scale of zero counts as one, and the
+// page's values as zeros.)  Both references are lazy: raised only when passed
+// by 2^12.
+//
+// Bound by the softmax threads' chain per page (as the other 128-row kernel
+// of this library is); the widening takes three warps' spare issue slots.
+
+constexpr int kTileRows = 128;
+constexpr int kRowsThreads = 384;               // 12 warps, three per scheduler: 168 registers a thread
+constexpr int kWideners = 96;
+constexpr int kKvStages = 2, kSBufs = 2;        // steps in shared memory, and in S buffers
+constexpr float kLazy = 12.f;
+constexpr float kLeastScale = 1.17549435e-38f;  // a value scale below the normal range counts as zero
+constexpr uint32_t kStep = 32768;               // 128 keys x 128 columns of fp16
+constexpr uint32_t kRowsOffK = kStep, kRowsOffV = kRowsOffK + kKvStages * kStep;
+constexpr uint32_t kRowsOffMisc = kRowsOffV + kKvStages * kStep;
+constexpr int kRowsSmem = (int)kRowsOffMisc + 4096 + 1024;      // + alignment of the tiles
+constexpr uint32_t kColO = 256;                 // S buffers at 0 and 128; accumulators at 256, 256 + d
+
+enum : int {
+  kBarQFull = 0, kBarQEmpty, kBarKFull, kBarKEmpty = kBarKFull + kKvStages, kBarVFull = kBarKEmpty + kKvStages,
+  kBarVEmpty = kBarVFull + kKvStages, kBarSFull = kBarVEmpty + kKvStages,
+  kBarPFull = kBarSFull + kSBufs,               // [2 halves][kSBufs]
+  kBarSFree = kBarPFull + 2 * kSBufs, kBarOFull = kBarSFree + kSBufs, kBarOEmpty, kBarEnd, kBars
+};
+
+struct RowsMisc {
+  uint64_t bar[kBars];
+  uint32_t tmem, abort;
+  float fac[kTileRows];
+  float xch[2][3][kTileRows];                   // of each half: reference of y, of s, row sum
+};
+static_assert(sizeof(RowsMisc) <= 4096, "misc region");
+
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// The CTA's segments, in the order that every role walks them.
+struct Segments {
+  Shares sh;
+  unsigned u, u_end, before;
+  int seq;
+  // a warp calls; false: nothing for this CTA
+  __device__ bool init(const AttnArgs& p) {
+    sh = shares_of(p);
+    if ((int)blockIdx.x >= sh.ctas) return false;
+    u = sh.first(blockIdx.x);
+    u_end = sh.first(blockIdx.x + 1);
+    seq = 0;
+    before = 0;
+    if (!p.whole) find_sequence(p, u, &seq, &before);
+    return true;
+  }
+  __device__ bool next(const AttnArgs& p, Segment* s, int* len, bool* starts, bool* whole) {
+    if (u >= u_end) return false;
+    int units;
+    item_of(p, u, seq, before, s, &units);
+    *starts = s->j0 == 0;
+    s->j1 = (int)min((unsigned)units, s->j0 + (u_end - u));
+    *whole = *starts && s->j1 == units;
+    u += s->j1 - s->j0;
+    if (!p.whole && u - before == (unsigned)units * p.c.heads * p.tiles) {
+      before = u;
+      seq += 1;
+    }
+    *len = seq_len(p, s->b);
+    if (p.whole) s->j1 = blocks_of(*len);
+    return true;
+  }
+};
+
+// The page of block j, or -1 (an empty sequence, a page out of range).
+__device__ __forceinline__ int page_of(const AttnArgs& p, int b, int j, int len) {
+  if (len <= 0) return -1;
+  const int page = __ldg(p.c.table + (long long)b * p.c.max_blocks + j);
+  return (unsigned)page < (unsigned)p.c.n_pages ? page : -1;
+}
+
+template <int D, typename T, bool I8>
+__global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const __grid_constant__ AttnArgs p) {
+  using namespace tc;
+  constexpr int KSTEPS = D / 16;
+  extern __shared__ unsigned char rows_mem[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)rows_mem + 1023) & ~(uintptr_t)1023);
+  RowsMisc* ms = reinterpret_cast<RowsMisc*>(smem + kRowsOffMisc);
+  const uint32_t sbase = su32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile uint32_t* dead = &ms->abort;
+  auto bar = [&](int i) { return su32(&ms->bar[i]); };
+
+  cudaTriggerProgrammaticLaunchCompletion();
+  Segments walk;
+  if (!walk.init(p)) return;                    // uniform over the CTA
+  if (tid == 0) {
+    mbar_init(bar(kBarQFull), 1);
+    mbar_init(bar(kBarQEmpty), 1);
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(bar(kBarKFull + i), kWideners / 32);
+      mbar_init(bar(kBarKEmpty + i), 1);
+      mbar_init(bar(kBarVFull + i), kWideners / 32);
+      mbar_init(bar(kBarVEmpty + i), 1);
+    }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(bar(kBarSFull + i), 1);
+      mbar_init(bar(kBarPFull + i), 4);          // the first warpgroup
+      mbar_init(bar(kBarPFull + kSBufs + i), 4);
+      mbar_init(bar(kBarSFree + i), 1);
+    }
+    mbar_init(bar(kBarOFull), 1);
+    mbar_init(bar(kBarOEmpty), 8);
+    mbar_init(bar(kBarEnd), 1);
+    ms->abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    for (int b = blockIdx.x; b < p.c.B; b += walk.sh.ctas) {      // lengths out of range are clamped, and recorded
+      const int n = __ldg(p.c.len + b);
+      if (n < 0 || n > p.c.max_blocks * kBlock) atomicOr(&g_cattn_flags, kFlagIndex);
+    }
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&ms->tmem)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  Segment s;
+  int len;
+  bool starts, whole;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t ID_S = idesc_f16(false, false, false, 128, 128);   // Q . K^T
+      constexpr uint32_t ID_O = idesc_f16(false, false, true, D, 128);      // P . V, V MN-major
+      const uint64_t dQ = sdesc(sbase, 16, 1024);
+      const uint64_t dK = sdesc(sbase + kRowsOffK, 16, 1024);
+      const uint64_t dV = sdesc(sbase + kRowsOffV, 16384, 1024);
+      uint32_t n = 0, item = 0;                 // steps before this item; items
+      bool ok = true;
+      while (ok && walk.next(p, &s, &len, &starts, &whole)) {
+        ok = wait_bar(bar(kBarQFull), item & 1u, dead, 101);
+        const uint32_t first = n, end = n + (uint32_t)max((s.j1 - s.j0 + 1) / 2, 1);
+        // S runs one step ahead of P V
+        for (uint32_t x = first; ok && x <= end; ++x) {
+          if (x < end) {
+            const uint32_t st = x % kKvStages, sb = x % kSBufs;
+            ok = wait_bar(bar(kBarKFull + st), (x / kKvStages) & 1u, dead, 102) &&
+                 wait_bar(bar(kBarSFree + sb), ((x / kSBufs) & 1u) ^ 1u, dead, 103);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b0 = dK + ((st * kStep) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < KSTEPS; ++kk) {
+              const uint32_t off = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              umma_f16(tmem + sb * 128, dQ + off, b0 + off, ID_S, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(bar(kBarKEmpty + st));
+            umma_commit(bar(kBarSFull + sb));
+            if (x == end - 1) umma_commit(bar(kBarQEmpty));
+          }
+          if (x > first) {
+            const uint32_t y = x - 1, st = y % kKvStages, sb = y % kSBufs;
+            ok = wait_bar(bar(kBarVFull + st), (y / kKvStages) & 1u, dead, 104) &&
+                 (y > first || wait_bar(bar(kBarOEmpty), (item & 1u) ^ 1u, dead, 105));
+            const uint64_t b0 = dV + ((st * kStep) >> 4);
+#pragma unroll
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = wait_bar(bar(kBarPFull + h * kSBufs + sb), (y / kSBufs) & 1u, dead, 106);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f16_ts(tmem + kColO + h * D, tmem + sb * 128 + 64 * h + kk * 8, b0 + (uint32_t)(((4 * h + kk) * 2048) >> 4),
+                            ID_O, (y > first || kk > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            umma_commit(bar(kBarVEmpty + st));
+            umma_commit(bar(kBarSFree + sb));
+          }
+        }
+        if (ok) umma_commit(bar(kBarOFull));
+        n = end;
+        ++item;
+      }
+      // every MMA issued here has finished before the tensor memory is given back
+      umma_commit(bar(kBarEnd));
+      volatile uint32_t no_abort = 0u;
+      wait_bar(bar(kBarEnd), 0u, &no_abort, 107);
+    }
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- widening
+    // A tile is a page's K or V: of a step K of both pages, then V of both.
+    // Thread t takes a 16-byte piece of row r0 + RPP i, the pieces laid over
+    // the lanes so that the fp16 stores (swizzled) meet no bank twice.
+    constexpr int CPR = D / 16;                  // pieces of a row of codes
+    constexpr int RPP = kWideners / CPR;         // rows per pass
+    constexpr int P = (kBlock + RPP - 1) / RPP;  // passes: 6 (d = 128) or 3 (d = 64)
+    const int t = tid - 32;
+    const int cc = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
+    const int r0 = D == 128 ? (t >> 2 & 1) | (t >> 3 & 2) | (t >> 5 << 2) : t >> 2;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && walk.next(p, &s, &len, &starts, &whole)) {
+      uint4 b0[P], b1[P], b2[P];                 // the tile at hand and the two after it
+      float z0 = 1.f, z1 = 1.f, z2 = 1.f;        // their value scales (1 for keys)
+      auto load = [&](uint4 (&to)[P], float& scale, int w, int j, int page) {   // (zeros for a page that is not there)
+        scale = 1.f;
+        if (page < 0) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) to[i] = make_uint4(0u, 0u, 0u, 0u);
+          return;
+        }
+        const long long cell = (long long)page * p.c.heads + s.h;
+        const uint4* src = static_cast<const uint4*>(w ? p.c.v : p.c.k) + cell * (kBlock * CPR) + r0 * CPR + cc;
+        const int rows = w ? min(len - j * kBlock, kBlock) : kBlock;       // V rows past the sequence: zeros
+#pragma unroll
+        for (int i = 0; i < P; ++i) to[i] = r0 + RPP * i < rows ? __ldg(src + i * RPP * CPR) : make_uint4(0u, 0u, 0u, 0u);
+        if (w) scale = __ldg(p.c.v_scale + cell);
+      };
+      auto number = [&](int j) {                 // the page of block j of the segment
+        if (j >= s.j1) return -1;
+        const int page = page_of(p, s.b, j, len);
+        return page;
+      };
+      int g0 = number(s.j0), g1 = number(s.j0 + 1);
+      load(b0, z0, 0, s.j0, g0);
+      load(b1, z1, 0, s.j0 + 1, g1);
+      for (int j = s.j0; j < max(s.j1, s.j0 + 1); j += 2, ++n) {
+        if (len > 0 && t == 0 && (g0 < 0 || (j + 1 < s.j1 && g1 < 0))) atomicOr(&g_cattn_flags, kFlagIndex);
+        const int n0 = number(j + 2), n1 = number(j + 3);
+        const uint32_t st = n % kKvStages;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int w = q >> 1, e = q & 1;
+          // two tiles ahead
+          if (q < 2) load(b2, z2, 1, j + q, q ? g1 : g0);
+          else load(b2, z2, 0, j + q, q == 2 ? n0 : n1);
+          if (e == 0) {
+            ok = wait_bar(bar((w ? kBarVEmpty : kBarKEmpty) + st), ((n / kKvStages) & 1u) ^ 1u, dead, 108 + w);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          if (!(z0 >= kLeastScale)) {            // a value scale of zero: zeros
+#pragma unroll
+            for (int i = 0; i < P; ++i) b0[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          const uint32_t to = sbase + (w ? kRowsOffV : kRowsOffK) + st * kStep + (uint32_t)(cc >> 2) * 16384 + e * 8192;
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int r = r0 + RPP * i;
+            if (r < kBlock) {
+              uint32_t x[8];
+              Widen<I8>::word(b0[i].x, x[0], x[1]);
+              Widen<I8>::word(b0[i].y, x[2], x[3]);
+              Widen<I8>::word(b0[i].z, x[4], x[5]);
+              Widen<I8>::word(b0[i].w, x[6], x[7]);
+              const uint32_t at = to + r * 128 + ((((cc & 3) * 2) ^ (r & 7)) << 4);
+              st_shared_v4(at, x[0], x[1], x[2], x[3]);
+              st_shared_v4(at ^ 16u, x[4], x[5], x[6], x[7]);
+            }
+          }
+          if (e == 1) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar((w ? kBarVFull : kBarKFull) + st));
+          }
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            b0[i] = b1[i];
+            b1[i] = b2[i];
+          }
+          z0 = z1;
+          z1 = z2;
+        }
+        if (!ok) break;
+        g0 = n0;
+        g1 = n1;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int wq = warp & 3, half = warp >= 8 ? 1 : 0, row = wq * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t own = tmem + lane_off + kColO + half * D;      // this half's accumulator
+    constexpr int DH = D / 2;                    // columns this thread stores
+    uint32_t n = 0, item = 0;
+    bool stop = false;
+    while (walk.next(p, &s, &len, &starts, &whole)) {
+      // Q of the item: two threads per row, fp16 under the row's power of two
+      stop = !wait_bar(bar(kBarQEmpty), (item & 1u) ^ 1u, dead, 110);
+      {
+        const int qi = tid - 128, qr = qi >> 1, hf = qi & 1;
+        int t, hg;
+        const bool live = row_of<kTileRows>(p, s, qr, &t, &hg);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const T*>(p.q) + (((long long)s.b * p.heads_q + s.h * p.group + hg) * p.Tq + t) * D + hf * DH);
+        uint4 raw[DH / 8];
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        auto pair = [&](int i) {
+          const uint32_t w = reinterpret_cast<const uint32_t*>(raw)[i];
+          if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+          else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        };
+        float amax = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < DH / 2; ++i) {
+          const float2 f = pair(i);
+          odd = odd || !(fabsf(f.x) < INFINITY) || !(fabsf(f.y) < INFINITY);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        odd = (__ballot_sync(0xffffffffu, odd) >> (lane & ~1)) & 3u;
+        int e = (int)(__float_as_uint(amax) >> 23) - 127;
+        e = min(max(e, -126), 126);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) {
+          uint32_t x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = pair(4 * i + k);
+            x[k] = h2bits(__floats2half2_rn(f.x * down, f.y * down));
+          }
+          const int d0 = hf * DH + 8 * i;
+          st_shared_v4(sbase + (d0 / 64) * 16384 + qr * 128 + (((d0 % 64 / 8) ^ (qr & 7)) << 4), x[0], x[1], x[2], x[3]);
+        }
+        if (hf == 0)
+          ms->fac[qr] = odd ? __int_as_float(0x7fffffff)
+                            : __uint_as_float((uint32_t)(127 + e) << 23) *
+                                  (1.44269504088896340736f / (D == 64 ? 8.f : 11.31370849898476039041f));
+        fence_async_smem();
+      }
+      if (named_bar_or(1, 256, stop)) {          // all eight warps agree
+        stop = true;
+        break;
+      }
+      if (tid == 128) mbar_arrive(bar(kBarQFull));
+      const float fac = ms->fac[row];
+      int t, hg;
+      const bool live = row_of<kTileRows>(p, s, row, &t, &hg);
+      const int lim = live && p.causal ? max(len - p.Tq + 1 + t, 0) : len;
+
+      float ry = 0.f, rs = 0.f, l = 0.f;         // references of y and s (log2), row sum against rs
+      bool have = false;
+      // page j's scales and first token, one step ahead
+      auto scales = [&](int j, float* ks, float* vs, int* tok) {
+        *ks = *vs = 0.f;
+        *tok = 1 << 30;
+        if (j < s.j1) {
+          const int page = page_of(p, s.b, j, len);
+          if (page >= 0) {
+            const long long cell = (long long)page * p.c.heads + s.h;
+            *ks = __ldg(p.c.k_scale + cell);
+            *vs = __ldg(p.c.v_scale + cell);
+            *tok = j * kBlock;
+          }
+        }
+      };
+      float ks, vs, ks_n, vs_n;
+      int tok, tok_n;
+      scales(s.j0 + half, &ks, &vs, &tok);
+      const int steps = max((s.j1 - s.j0 + 1) / 2, 1);      // (a page that is not there is masked)
+      for (int i = 0; i < steps; ++i) {
+        const uint32_t x = n + (uint32_t)i, sb = x % kSBufs;
+        scales(s.j0 + 2 * (i + 1) + half, &ks_n, &vs_n, &tok_n);
+        if (!__all_sync(0xffffffffu, wait_bar(bar(kBarSFull + sb), (x / kSBufs) & 1u, dead, 111))) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        float v[64];
+        tmem_ld32(tmem + lane_off + sb * 128 + 64 * half, v);
+        tmem_ld32(tmem + lane_off + sb * 128 + 64 * half + 32, v + 32);
+        tmem_wait_ld();
+        const float f = fac * ks, lv = vs >= kLeastScale ? __log2f(vs) : 0.f;
+        // the largest s of the row (log2 units; f >= 0)
+        const bool edge = !__all_sync(0xffffffffu, tok + kBlock <= lim);
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) v[c] = tok + c < lim ? v[c] * f : -INFINITY;
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 64; c += 8) {
+          m0 = max3(m0, v[c], v[c + 1]);
+          m1 = max3(m1, v[c + 2], v[c + 3]);
+          m2 = max3(m2, v[c + 4], v[c + 5]);
+          m3 = max3(m3, v[c + 6], v[c + 7]);
+        }
+        const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+        const float smax = edge ? top : top * f;
+        float alpha = 1.f;
+        if (smax > -INFINITY) {
+          const float ymax = smax + lv;
+          if (!have) {
+            ry = ymax;
+            rs = smax;
+            have = true;
+          } else {
+            if (ymax > ry + kLazy) {
+              alpha = ex2(ry - ymax);
+              ry = ymax;
+            }
+            if (smax > rs + kLazy) {
+              l *= ex2(rs - smax);
+              rs = smax;
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          // rescale this half's accumulator (factor 1 where nothing changed)
+          // once its previous P V product is done; there is one, in this item
+          const uint32_t xp = x - 1u, sp = xp % kSBufs;
+          if (!__all_sync(0xffffffffu, wait_bar(bar(kBarSFree + sp), (xp / kSBufs) & 1u, dead, 112))) {
+            stop = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            float o[32];
+            tmem_ld32(own + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] *= alpha;
+            tmem_st32(own + c0, o);
+          }
+          tmem_wait_st();
+        }
+        // P = 2^(s + lv - ry) as fp16 pairs over the first 32 of this half's 64 S columns
+        uint32_t pk[32];
+        const float shift = lv - ry;
+        const F2 ff = edge ? f2(1.f, 1.f) : f2(f, f), zz = f2(shift, shift);
+        F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          float e0, e1, e2, e3;
+          split2(fma2(f2(v[c], v[c + 1]), ff, zz), e0, e1);
+          split2(fma2(f2(v[c + 2], v[c + 3]), ff, zz), e2, e3);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          e2 = ex2(e2);
+          e3 = ex2(e3);
+          sum0 = add2(sum0, f2(e0, e1));
+          sum1 = add2(sum1, f2(e2, e3));
+          pk[c / 2] = pack_f16x2(e0, e1);
+          pk[c / 2 + 1] = pack_f16x2(e2, e3);
+        }
+        tmem_st32u(tmem + lane_off + sb * 128 + 64 * half, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + half * kSBufs + sb));
+        float a0, a1;
+        split2(add2(sum0, sum1), a0, a1);
+        // sum of 2^(s - rs)
+        l += (a0 + a1) * ex2(ry - lv - rs);
+        ks = ks_n;
+        vs = vs_n;
+        tok = tok_n;
+      }
+      n += (uint32_t)steps;
+
+      // the two halves, merged; then this thread's half of the columns
+      const bool ok = !stop && __all_sync(0xffffffffu, wait_bar(bar(kBarOFull), item & 1u, dead, 113));
+      ms->xch[half][0][row] = ry;
+      ms->xch[half][1][row] = rs;
+      ms->xch[half][2][row] = l;
+      if (named_bar_or(1, 256, !ok)) {           // all eight warps agree
+        stop = true;
+        break;
+      }
+      ++item;
+      tc_fence_after();
+      const float yA = ms->xch[0][0][row], sA = ms->xch[0][1][row], lA = ms->xch[0][2][row];
+      const float yB = ms->xch[1][0][row], sB = ms->xch[1][1][row], lB = ms->xch[1][2][row];
+      // (a half without a key has l = 0 and takes no part; NaN stays)
+      const float top = fmaxf(lA != 0.f ? sA : -INFINITY, lB != 0.f ? sB : -INFINITY);
+      const float z = top == -INFINITY ? 0.f : top;
+      const float wA = lA != 0.f ? ex2(yA - z) : 0.f, wB = lB != 0.f ? ex2(yB - z) : 0.f;
+      const float sum = (lA != 0.f ? lA * ex2(sA - z) : 0.f) + (lB != 0.f ? lB * ex2(sB - z) : 0.f);
+      float* const part = p.part + ((2LL * blockIdx.x + (starts ? 1 : 0)) * kTileRows + row) * D;
+#pragma unroll
+      for (int c0 = 0; c0 < DH; c0 += 16) {
+        float oa[16], ob[16];
+        tmem_ld16(tmem + lane_off + kColO + half * DH + c0, oa);
+        tmem_ld16(tmem + lane_off + kColO + D + half * DH + c0, ob);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            float r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = (lA != 0.f ? oa[c + k] * wA : 0.f) + (lB != 0.f ? ob[c + k] * wB : 0.f);
+            const int col = half * DH + c0 + c;
+            const float4 x4 = make_float4(r[0], r[1], r[2], r[3]);
+            // (kShift: the joining kernel's sums are held times 2^kShift)
+            if (whole) write_out<D, T>(p, s, t, hg, col, x4, top + kShift, sum);
+            else *reinterpret_cast<float4*>(part + col) = x4;
+          }
+        }
+      }
+      if (!whole && live && half == 0) {
+        float* st = p.part + 2LL * p.grid * kTileRows * D + ((2LL * blockIdx.x + (starts ? 1 : 0)) * kTileRows + row) * 2;
+        st[0] = top + kShift;
+        st[1] = sum;
+      }
+      // the accumulators, and the exchanged values, are free for the next item
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarOEmpty));
+      named_bar(2, 256);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+  }
+}

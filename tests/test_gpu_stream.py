@@ -794,3 +794,70 @@ def test_sparse_layer_with_norm_and_rotation(order):
         got.forward_host(q, k, v, o)
     with pytest.raises(ValueError):
         got(q, k, x[:, :, 2 * h:].transpose(1, 2))         # a view as v
+
+
+# ---- many query rows per key head -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,heads,group,Tq,d,dtype,code", [
+    ([64], 1, 1, 33, 128, BF, "i8"),             # one page, rows that see little
+    ([20, 0, 130], 1, 1, 40, 64, HF, "e4m3"),    # more queries than keys, an empty sequence
+    ([300], 2, 1, 128, 128, HF, "e4m3"),         # one full tile
+    ([700, 64, 65], 1, 1, 129, 64, BF, "i8"),    # one row past a tile
+    ([2100], 1, 3, 111, 128, BF, "e4m3"),        # several tiles, shared over CTAs
+    ([1300, 5], 2, 40, 2, 64, HF, "i8"),         # a wide group
+])
+def test_attention_of_many_rows_matches_the_oracle(lens, heads, group, Tq, d, dtype, code, causal):
+    gpu = _filled(len(lens), heads, d, code, lens, blocks=max(1, -(-max(lens) // 64)) + 1)
+    q = torch.randn(len(lens), heads * group, Tq, d, generator=_gen(24)).to(dtype).cuda()
+    o, lse = gpu.attend(q, causal)
+    svsa.svsa_sync_status()
+    _check_attention(gpu, q, o, lse, causal)
+    again, _ = gpu.attend(q, causal, lse=False)
+    assert torch.equal(o, again)
+
+
+def test_many_rows_with_scales_of_any_size_and_rows_that_are_not_finite():
+    gpu = _filled(1, 1, 128, "i8", [1280])
+    pages = gpu.table[0, :20].long()
+    scale = torch.tensor([3e-20, 1e10, 0.3, 1.7e-5, 0.0, 2.0, 1e-30, 5e9, 1.0, 0.01], device="cuda")
+    gpu.v_scale[pages, 0] = torch.cat([scale, scale.flip(0) * 7])
+    gpu.k_scale[pages, 0] *= torch.linspace(0.0, 2.0, 20, device="cuda")
+    q = torch.randn(1, 3, 50, 128, generator=_gen(25)).to(BF)
+    q[0, 0, 7] *= 1e-20
+    q[0, 1, 3] = 0
+    q = q.cuda()
+    o, lse = gpu.attend(q)
+    _check_attention(gpu, q, o, lse, True)
+    # a few large contributions only: blocks of tiny values carry the rest
+    gpu.v_scale[pages, 0] = 1e-12
+    gpu.v_scale[pages[3], 0] = 1e12
+    gpu.k[pages[3], 0] = torch.full_like(gpu.k[pages[3], 0], -127)
+    gpu.k_scale[pages[3], 0] = 30.0
+    qp = q.abs()                                           # the page of huge values is 2^-1000 away for every row
+    o, lse = gpu.attend(qp)
+    _check_attention(gpu, qp, o, lse, True)
+    q[0, 2, 11, 5], q[0, 2, 12, 6] = float("inf"), float("nan")
+    gpu2 = _filled(1, 1, 128, "e4m3", [200])
+    o, lse = gpu2.attend(q)
+    bad = torch.zeros(1, 3, 50, dtype=torch.bool, device="cuda")
+    bad[0, 2, 11:13] = True
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all() and torch.isfinite(o[~bad].float()).all()
+
+
+def test_many_rows_leave_out_pages_out_of_range():
+    gpu = _filled(2, 1, 64, "e4m3", [500, 100], blocks=8)
+    q = torch.randn(2, 4, 30, 64, generator=_gen(26)).to(BF).cuda()
+    good = gpu.table.clone()
+    gpu.table[0, 3], gpu.table[0, 5] = -1, gpu.k.shape[0]
+    o, lse = gpu.attend(q, causal=False)
+    _index_error()
+    gpu.table.copy_(good)
+    lists = np.empty((2, 30, 1), dtype=object)
+    for t in range(30):
+        lists[0, t, 0], lists[1, t, 0] = [0, 1, 2, 4, 6, 7], [0, 1]
+    _check_attention(gpu, q, o, lse, False, lists)
+    gpu.len.copy_(torch.tensor([-3, 10000], dtype=torch.int32))
+    o, lse = gpu.attend(q)
+    _index_error()
+    assert torch.all(o[0] == 0)

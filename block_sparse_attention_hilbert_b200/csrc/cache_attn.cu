@@ -13,13 +13,16 @@
 // fp16 is exact, fp16 x fp16 products are exact in fp32), and up to eight
 // query rows cost half of what a tile of 16 query rows would.
 //
+// More than 32 (d = 64: 48) query rows per key head take the 128-row tcgen05
+// tiles of cache_attn_rows.cuh instead, over the same items and shares.
+//
 // Work: an item is (sequence, key head, tile of 8 or 16 rows), or with lists
 // (sequence, query, key head, tile of the group's rows); a unit is one
 // 64-token block of an item.  The CTAs, one per SM, take equal contiguous
 // shares of all units, so ragged lengths balance; an item that several CTAs
 // share is joined by a second kernel from fp32 partial sums with their maxima,
 // in CTA order.  Where items are short, or so many that whole ones balance,
-// each goes to one CTA and there is no second kernel.  In a CTA, eight warps
+// each goes to one CTA and there is no second kernel.  In a CTA, twelve warps (eight with 16 rows)
 // take the blocks of a segment in turn, each with a ring of its own of tiles
 // filled by TMA (128-byte swizzle, so that both the row-wise reads of K and
 // the column-wise reads of V are free of bank conflicts), and no barrier until
@@ -46,7 +49,6 @@ static __device__ unsigned int g_cattn_flags;
 namespace {
 
 constexpr float kShift = 14.f;              // weights are held times 2^kShift
-constexpr int kMaxSmallRows = 32;           // rows per key head up to which 16-row tiles are used
 constexpr int kMinUnits = 8;                // blocks of a CTA at least, where there are as many
 
 struct AttnArgs {
@@ -834,15 +836,20 @@ cudaError_t run_rows(const AttnArgs& p, cudaStream_t st) {
   return e != cudaSuccess || p.whole ? e : join<D, T, kTileRows>(p, st);
 }
 
-// Rows of a tile for this many query rows per key head (whole cache) or per
-// list.  ROWS_NOTE
-int tile_rows(long long rows, bool lists) { return rows <= 8 ? 8 : rows <= kMaxSmallRows || lists ? 16 : kTileRows; }
+// Rows of a tile for this many query rows per key head (or per list).  16-row
+// tiles widen the codes again for each, 128-row tiles cost the same for one
+// row as for 128.  32 rows over 4 caches of 60-65k tokens, d = 128: two 16-row
+// tiles 189 us, one of 128 rows 218 us, so three 16-row tiles would lose; d =
+// 64: 112 and 176 us, so four would.
+int tile_rows(long long rows, bool lists, int d) {
+  return rows <= 8 ? 8 : lists || rows <= (d == 128 ? 32 : 48) ? 16 : kTileRows;
+}
 
 }  // namespace
 
 size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq) {
   // (with or without lists: the larger)
-  const int rows = tile_rows((long long)heads_q / c.heads * Tq, false);
+  const int rows = tile_rows((long long)heads_q / c.heads * Tq, false, c.d);
   return (size_t)kNumSMs * 2 * std::max(rows, 16) * (c.d + 2) * sizeof(float);
 }
 
@@ -863,7 +870,7 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   p.cap = cap;
   p.group = heads_q / c.heads;
   const long long rows = idx ? p.group : (long long)p.group * Tq;
-  const int tile = tile_rows(rows, idx != nullptr);
+  const int tile = tile_rows(rows, idx != nullptr, c.d);
   p.tiles = ceil_div(rows, tile);
   p.grid = kNumSMs;
   // Whole items per CTA where no item is longer than two rounds of the warps,
@@ -902,7 +909,7 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
 // Units of one call at most (32-bit counters).
 long long cache_attn_units(const CacheArgs& c, int heads_q, int Tq, const int32_t* idx, int cap) {
   const long long group = heads_q / c.heads, rows = idx ? group : group * Tq;
-  const int tile = tile_rows(rows, idx != nullptr);
+  const int tile = tile_rows(rows, idx != nullptr, c.d);
   return (long long)c.B * (idx ? Tq : 1) * c.heads * ((rows + tile - 1) / tile) * (idx ? cap : c.max_blocks);
 }
 

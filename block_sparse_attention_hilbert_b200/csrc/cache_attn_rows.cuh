@@ -12,9 +12,10 @@
 // Roles: warp 0 issues the MMAs; warps 4-11 are two softmax warpgroups, one
 // thread per query row each, one for each page of a step, with a maximum, a
 // row sum and an accumulator of their own, merged at the item's end; warps
-// 1-3 widen the pages (loads two tiles ahead in registers).  (One page to a
-// step, with the same roles, left the issuing thread's waits the bound: 694 us
-// where this takes FRAME us, 1560 queries x 12 heads over 32,760 tokens.)
+// 1-3 and 12-15 widen the pages.  Measured on 1560 queries x
+// 12 heads over 32,760 tokens: 694 us with one page to a step, 645 with two,
+// 625 with seven widening warps for three and their loads through shared
+// memory, 554 (567 TFLOP/s) with the next step's K widened before this one's V.
 //
 // Scales: the key scale joins the softmax's factor.  The value scale goes
 // into the weights as an exponent, P = 2^(y - m'), y = s + log2 vs, with a
@@ -24,18 +25,20 @@
 // page's values as zeros.)  Both references are lazy: raised only when passed
 // by 2^12.
 //
-// Bound by the softmax threads' chain per page (as the other 128-row kernel
-// of this library is); the widening takes three warps' spare issue slots.
+// Bound by the hand-offs of a step (widen, S, softmax, P V): without the
+// widening the same loop takes two thirds of the time.
 
 constexpr int kTileRows = 128;
-constexpr int kRowsThreads = 384;               // 12 warps, three per scheduler: 168 registers a thread
-constexpr int kWideners = 96;
+constexpr int kRowsThreads = 512;               // 16 warps, 128 registers a thread
+constexpr int kWideners = kRowsThreads - 288;   // warps 1-3 and 12 on
 constexpr int kKvStages = 2, kSBufs = 2;        // steps in shared memory, and in S buffers
 constexpr float kLazy = 12.f;
 constexpr float kLeastScale = 1.17549435e-38f;  // a value scale below the normal range counts as zero
 constexpr uint32_t kStep = 32768;               // 128 keys x 128 columns of fp16
 constexpr uint32_t kRowsOffK = kStep, kRowsOffV = kRowsOffK + kKvStages * kStep;
-constexpr uint32_t kRowsOffMisc = kRowsOffV + kKvStages * kStep;
+constexpr uint32_t kRowsOffRaw = kRowsOffV + kKvStages * kStep;
+constexpr int kRaw = 3;                         // stages of codes in flight
+constexpr uint32_t kRowsOffMisc = kRowsOffRaw + kRaw * 16384;
 constexpr int kRowsSmem = (int)kRowsOffMisc + 4096 + 1024;      // + alignment of the tiles
 constexpr uint32_t kColO = 256;                 // S buffers at 0 and 128; accumulators at 256, 256 + d
 
@@ -218,94 +221,116 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       volatile uint32_t no_abort = 0u;
       wait_bar(bar(kBarEnd), 0u, &no_abort, 107);
     }
-  } else if (warp < 4) {
+  } else if (warp < 4 || warp >= 12) {
     // ---------------------------------------------------------------- widening
-    // A tile is a page's K or V: of a step K of both pages, then V of both.
-    // Thread t takes a 16-byte piece of row r0 + RPP i, the pieces laid over
-    // the lanes so that the fp16 stores (swizzled) meet no bank twice.
+    // Stages of two pages' K or V, in the order in which they are needed: K of
+    // the next step before V of this one (V is read a softmax later).  Thread t
+    // takes the 16-byte pieces (r0 + RPP i, cc) of each page, laid over the
+    // lanes so that the fp16 stores (swizzled) meet no bank twice.  It copies
+    // them to a ring of kRaw stages in shared memory ahead of time and reads
+    // back its own bytes only, so the ring needs no barrier.
     constexpr int CPR = D / 16;                  // pieces of a row of codes
     constexpr int RPP = kWideners / CPR;         // rows per pass
-    constexpr int P = (kBlock + RPP - 1) / RPP;  // passes: 6 (d = 128) or 3 (d = 64)
-    const int t = tid - 32;
+    constexpr int P = (kBlock + RPP - 1) / RPP;
+    const int t = warp < 4 ? tid - 32 : tid - 288;
     const int cc = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
     const int r0 = D == 128 ? (t >> 2 & 1) | (t >> 3 & 2) | (t >> 5 << 2) : t >> 2;
+    const int piece = (r0 * CPR + cc) * 16;
     uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(p, &s, &len, &starts, &whole)) {
-      uint4 b0[P], b1[P], b2[P];                 // the tile at hand and the two after it
-      float z0 = 1.f, z1 = 1.f, z2 = 1.f;        // their value scales (1 for keys)
-      auto load = [&](uint4 (&to)[P], float& scale, int w, int j, int page) {   // (zeros for a page that is not there)
-        scale = 1.f;
-        if (page < 0) {
+      const int steps = (s.j1 - s.j0 + 1) / 2;   // (a page that is not there is zeros)
+      // stage g: K 0, K 1, V 0, K 2, V 1, ..., V steps - 1
+      auto is_v = [&](int g) { return g > 0 && ((g & 1) == 0 || g == 2 * steps - 1); };
+      auto step_of = [&](int g) { return g == 0 ? 0 : g & 1 ? min((g + 1) / 2, steps - 1) : g / 2 - 1; };
+      auto number = [&](int g, int e) {          // the page of stage g's half e
+        const int j = s.j0 + 2 * step_of(g) + e;
+        return g < 2 * steps && j < s.j1 ? page_of(p, s.b, j, len) : -1;
+      };
+      auto scale = [&](int g, int page) {        // its value scale (1 where there is none to look at)
+        return g < 2 * steps && is_v(g) && page >= 0 ? __ldg(p.c.v_scale + (long long)page * p.c.heads + s.h) : 1.f;
+      };
+      // stage g, of the pages p0 and p1 (-1: zeros), into the ring's place `slot`; V rows past the sequence: zeros
+      auto ask = [&](int g, int p0, int p1, uint32_t slot) {
+        if (g < 2 * steps) {
+          const int v = is_v(g), j = s.j0 + 2 * step_of(g);
 #pragma unroll
-          for (int i = 0; i < P; ++i) to[i] = make_uint4(0u, 0u, 0u, 0u);
-          return;
+          for (int e = 0; e < 2; ++e) {
+            const int page = e ? p1 : p0;
+            const char* src = static_cast<const char*>(v ? p.c.v : p.c.k) +
+                              (size_t)(unsigned)(max(page, 0) * p.c.heads + s.h) * (kBlock * D) + piece;
+            const uint32_t to = sbase + kRowsOffRaw + slot * 16384 + e * (kBlock * D) + piece;
+            const int rows = page < 0 ? 0 : v ? min(len - (j + e) * kBlock, kBlock) : kBlock;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              if (r0 + RPP * i < kBlock)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to + i * RPP * D), "l"(src + i * RPP * D),
+                             "r"(r0 + RPP * i < rows ? 16 : 0) : "memory");
+          }
         }
-        const long long cell = (long long)page * p.c.heads + s.h;
-        const uint4* src = static_cast<const uint4*>(w ? p.c.v : p.c.k) + cell * (kBlock * CPR) + r0 * CPR + cc;
-        const int rows = w ? min(len - j * kBlock, kBlock) : kBlock;       // V rows past the sequence: zeros
-#pragma unroll
-        for (int i = 0; i < P; ++i) to[i] = r0 + RPP * i < rows ? __ldg(src + i * RPP * CPR) : make_uint4(0u, 0u, 0u, 0u);
-        if (w) scale = __ldg(p.c.v_scale + cell);
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
       };
-      auto number = [&](int j) {                 // the page of block j of the segment
-        if (j >= s.j1) return -1;
-        const int page = page_of(p, s.b, j, len);
-        return page;
-      };
-      int g0 = number(s.j0), g1 = number(s.j0 + 1);
-      load(b0, z0, 0, s.j0, g0);
-      load(b1, z1, 0, s.j0 + 1, g1);
-      for (int j = s.j0; j < max(s.j1, s.j0 + 1); j += 2, ++n) {
-        if (len > 0 && t == 0 && (g0 < 0 || (j + 1 < s.j1 && g1 < 0))) atomicOr(&g_cattn_flags, kFlagIndex);
-        const int n0 = number(j + 2), n1 = number(j + 3);
-        const uint32_t st = n % kKvStages;
+      float z[kRaw][2];
+      uint32_t slot = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int w = q >> 1, e = q & 1;
-          // two tiles ahead
-          if (q < 2) load(b2, z2, 1, j + q, q ? g1 : g0);
-          else load(b2, z2, 0, j + q, q == 2 ? n0 : n1);
-          if (e == 0) {
-            ok = wait_bar(bar((w ? kBarVEmpty : kBarKEmpty) + st), ((n / kKvStages) & 1u) ^ 1u, dead, 108 + w);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
-          if (!(z0 >= kLeastScale)) {            // a value scale of zero: zeros
+      for (int i = 0; i < kRaw; ++i) {
+        const int p0 = number(i, 0), p1 = number(i, 1);
+        z[i][0] = scale(i, p0);
+        z[i][1] = scale(i, p1);
+        ask(i, p0, p1, i);
+      }
+      int p0 = number(kRaw, 0), p1 = number(kRaw, 1);
+      for (int g = 0; g < 2 * steps; ++g) {
+        const int v = is_v(g);
+        const uint32_t x = n + (uint32_t)step_of(g), st = x % kKvStages;
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kRaw - 1) : "memory");
+        ok = wait_bar(bar((v ? kBarVEmpty : kBarKEmpty) + st), ((x / kKvStages) & 1u) ^ 1u, dead, 108 + v);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < P; ++i) b0[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          const uint32_t to = sbase + (w ? kRowsOffV : kRowsOffK) + st * kStep + (uint32_t)(cc >> 2) * 16384 + e * 8192;
+        for (int e = 0; e < 2; ++e) {
+          const bool none = !(z[0][e] >= kLeastScale);      // (a value scale of zero: zeros)
+          const uint32_t from = sbase + kRowsOffRaw + slot * 16384 + e * (kBlock * D) + piece;
+          const uint32_t to = sbase + (v ? kRowsOffV : kRowsOffK) + st * kStep + (uint32_t)(cc >> 2) * 16384 + e * 8192 + r0 * 128;
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             const int r = r0 + RPP * i;
             if (r < kBlock) {
-              uint32_t x[8];
-              Widen<I8>::word(b0[i].x, x[0], x[1]);
-              Widen<I8>::word(b0[i].y, x[2], x[3]);
-              Widen<I8>::word(b0[i].z, x[4], x[5]);
-              Widen<I8>::word(b0[i].w, x[6], x[7]);
-              const uint32_t at = to + r * 128 + ((((cc & 3) * 2) ^ (r & 7)) << 4);
-              st_shared_v4(at, x[0], x[1], x[2], x[3]);
-              st_shared_v4(at ^ 16u, x[4], x[5], x[6], x[7]);
+              uint4 c = lds128(from + i * RPP * D);
+              if (none) c = make_uint4(0u, 0u, 0u, 0u);
+              uint32_t y[8];
+              Widen<I8>::word(c.x, y[0], y[1]);
+              Widen<I8>::word(c.y, y[2], y[3]);
+              Widen<I8>::word(c.z, y[4], y[5]);
+              Widen<I8>::word(c.w, y[6], y[7]);
+              const uint32_t at = to + RPP * i * 128 + ((((cc & 3) * 2) ^ (r & 7)) << 4);
+              st_shared_v4(at, y[0], y[1], y[2], y[3]);
+              st_shared_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
             }
           }
-          if (e == 1) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar((w ? kBarVFull : kBarKFull) + st));
-          }
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            b0[i] = b1[i];
-            b1[i] = b2[i];
-          }
-          z0 = z1;
-          z1 = z2;
         }
-        if (!ok) break;
-        g0 = n0;
-        g1 = n1;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar((v ? kBarVFull : kBarKFull) + st));
+        // the stage kRaw further on takes this one's place (its pages' numbers were read a stage ago)
+#pragma unroll
+        for (int i = 0; i + 1 < kRaw; ++i) {
+          z[i][0] = z[i + 1][0];
+          z[i][1] = z[i + 1][1];
+        }
+        z[kRaw - 1][0] = scale(g + kRaw, p0);
+        z[kRaw - 1][1] = scale(g + kRaw, p1);
+        ask(g + kRaw, p0, p1, slot);
+        p0 = number(g + kRaw + 1, 0);
+        p1 = number(g + kRaw + 1, 1);
+        slot = slot + 1 == kRaw ? 0 : slot + 1;
+      }
+      asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+      n += (uint32_t)steps;
+      if (len > 0 && ok) {                       // pages out of range, recorded
+        bool bad = false;
+        for (int j = s.j0 + t; j < s.j1; j += kWideners) bad = bad || page_of(p, s.b, j, len) < 0;
+        if (bad) atomicOr(&g_cattn_flags, kFlagIndex);
       }
     }
   } else {
@@ -450,13 +475,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
           }
           tc_fence_after();
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            float o[32];
-            tmem_ld32(own + c0, o);
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            float o[16];
+            tmem_ld16(own + c0, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] *= alpha;
-            tmem_st32(own + c0, o);
+            for (int c = 0; c < 16; ++c) o[c] *= alpha;
+            tmem_st16(own + c0, o);
           }
           tmem_wait_st();
         }

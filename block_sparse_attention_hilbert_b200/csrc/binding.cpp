@@ -86,6 +86,15 @@ int dtype_of(const at::Tensor& t, const char* name) {
 }
 at::ScalarType type_of(int dtype) { return dtype == SVSA_F16 ? at::kHalf : at::kBFloat16; }
 
+// A workspace and the bytes of it that the call may use.
+void* workspace(const at::Tensor* ws, int64_t bytes, int device) {
+  if (ws == nullptr) return nullptr;
+  if (ws->get_device() != device || !ws->is_contiguous() || bytes < 0 || (size_t)bytes > ws->nbytes())
+    fail("ws: expected a contiguous tensor of at least ws_bytes=" + std::to_string(bytes) + " bytes on device " +
+         std::to_string(device) + ", got " + got(*ws));
+  return ws->data_ptr();
+}
+
 int64_t integer(PyObject* o) {
   const long long v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw Fail{};
@@ -289,12 +298,12 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* pdk = r.k ? view(dk, r.type, {p.B, p.heads_k, p.N, p.d}, p.dk_stride, r.device, "dk") : nullptr;
     void* dwq = dense(tensor(a[12], "dwq", true), at::kFloat, {p.d}, r.device, "dwq");
     void* dwk = dense(tensor(a[13], "dwk", true), at::kFloat, {p.d}, r.device, "dwk");
-    const at::Tensor* ws = tensor(a[15], "ws", true);
+    const int64_t bytes = integer(a[16]);
+    void* ws = workspace(tensor(a[15], "ws", true), bytes, r.device);
     Launch l(r.device, a[17]);
     return PyLong_FromLong(svsa_qk_norm_rope_bwd(dyq, dyk, r.pq, r.pk, (float*)r.wq, (float*)r.wk, (float*)r.cos,
                                                  (float*)r.sin, (int32_t*)r.pos, (int32_t*)r.map, pdq, pdk, (float*)dwq,
-                                                 (float*)dwk, &p, ws ? ws->data_ptr() : nullptr, (size_t)integer(a[16]),
-                                                 l.stream()));
+                                                 (float*)dwk, &p, ws, (size_t)bytes, l.stream()));
   });
 }
 
@@ -429,10 +438,11 @@ PyObject* cache_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* cnt = dense(tensor(a[3], "cnt", true), at::kInt, {c->B, p->Tq, c->heads}, dev, "cnt");
     void* o = dense(tensor(a[4], "o"), type, {c->B, p->heads_q, p->Tq, c->d}, dev, "o");
     void* lse = dense(tensor(a[5], "lse", true), at::kFloat, {c->B, p->heads_q, p->Tq}, dev, "lse");
-    const at::Tensor* ws = tensor(a[7], "ws", true);
+    const int64_t bytes = integer(a[8]);
+    void* ws = workspace(tensor(a[7], "ws", true), bytes, dev);
     Launch l(dev, a[9]);
-    return PyLong_FromLong(svsa_cache_attn(&*c, q, (int32_t*)idx, (int32_t*)cnt, o, (float*)lse, &*p,
-                                           ws ? ws->data_ptr() : nullptr, (size_t)integer(a[8]), l.stream()));
+    return PyLong_FromLong(svsa_cache_attn(&*c, q, (int32_t*)idx, (int32_t*)cnt, o, (float*)lse, &*p, ws,
+                                           (size_t)bytes, l.stream()));
   });
 }
 

@@ -540,8 +540,9 @@ typedef enum {
 /* Keys and values of B sequences in 8 bits, in pages of one 64-token block:
  * token n of sequence b is row n % 64 of page table[b][n / 64], and stands for
  * code * scale, one scale per page and head.  A page may be read by several
- * sequences, but only one sequence may append to it.  Caller-owned device
- * memory. */
+ * sequences, but only one sequence may append to it, at one place of its
+ * table.  Codes within a sequence's length are not NaN (svsa_cache_append
+ * writes none).  Caller-owned device memory. */
 typedef struct {
   void* k;                    /* [n_pages, heads, 64, d] codes */
   void* v;

@@ -138,6 +138,12 @@ def test_cache_without_means_appends_and_attends_but_does_not_select():
     assert _attn(c, _query(), q=None) == 1 and "q is NULL" in _err()
 
 
+def test_append_of_more_tokens_than_fit_32_bits_of_blocks():
+    assert _append(_cache(B=1 << 20, heads=1 << 10), N=1 << 30) == 2
+    # (the most tokens that a call can name pass the size check, and fail at the pointer)
+    assert _append(_cache(B=1, heads=1), N=2**31 - 1, k=None) == 1 and "k is NULL" in _err()
+
+
 def test_append_rejects():
     c = _cache()
     for bad in (dict(N=0), dict(ks=(768, 384, 4)), dict(vs=(768, -384, 128)), dict(k=None), dict(v=161), dict(n_new=3),
@@ -213,6 +219,9 @@ def test_binding_checks_tensors():
         svsa.svsa_cache_attn(c, q.half(), None, None, q, None, qp, None, 0)
     with pytest.raises(ValueError):
         svsa.svsa_cache_attn(c, q, None, None, torch.empty_like(q).half(), None, qp, None, 0)
+    ws = torch.zeros(svsa.svsa_cache_attn_workspace_bytes(c, qp) - 1, dtype=torch.uint8)
+    with pytest.raises(ValueError):                        # fewer bytes than the call says
+        svsa.svsa_cache_attn(c, q, None, None, torch.empty_like(q), None, qp, ws, ws.numel() + 1)
     with pytest.raises(ValueError):
         svsa.svsa_cache_select(c, q, torch.zeros(2, 3, 2, 3, dtype=torch.int32), torch.zeros(2, 3, 2, dtype=torch.int32), qp)
 

@@ -99,7 +99,7 @@ cudaError_t launch_cache_append(const CacheArgs& c, const void* k, const void* v
 cudaError_t launch_cache_select(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal, int cap,
                                 int first, int last, int32_t* idx, int32_t* cnt, cudaStream_t st);
 cudaError_t cache_flags(unsigned int* v, cudaStream_t st);
-size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq);
+size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq, int cap);
 cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal,
                               const int32_t* idx, const int32_t* cnt, int cap, void* o, float* lse, void* ws,
                               int* launches, cudaStream_t st);
@@ -1138,10 +1138,13 @@ svsa_status svsa_cache_select(const svsa_cache* c, const void* q, int32_t* idx, 
 
 size_t svsa_cache_attn_workspace_bytes(const svsa_cache* c, const svsa_cache_query* p) {
   if (c == nullptr || p == nullptr || (c->d != 64 && c->d != 128) || c->heads < 1 || p->heads_q < 1 || p->Tq < 1) return 0;
+  if (c->B < 1 || c->max_blocks < 1 || p->heads_q % c->heads != 0 || (long long)c->B * p->heads_q * p->Tq >= (1LL << 27)) return 0;
   CacheArgs a{};
+  a.B = c->B;
   a.heads = c->heads;
   a.d = c->d;
-  return cache_attn_workspace_bytes(a, p->heads_q, p->Tq);
+  a.max_blocks = c->max_blocks;
+  return cache_attn_workspace_bytes(a, p->heads_q, p->Tq, p->cap);
 }
 
 svsa_status svsa_cache_attn(const svsa_cache* c, const void* q, const int32_t* idx, const int32_t* cnt, void* o,
@@ -1163,7 +1166,7 @@ svsa_status svsa_cache_attn(const svsa_cache* c, const void* q, const int32_t* i
   }
   const long long units = cache_attn_units(a, p->heads_q, p->Tq, idx, p->cap);
   if (units >= (1LL << 31)) return fail(SVSA_ERR_UNSUPPORTED, "%lld block visits exceed 2^31", units);
-  const size_t need = cache_attn_workspace_bytes(a, p->heads_q, p->Tq);
+  const size_t need = cache_attn_workspace_bytes(a, p->heads_q, p->Tq, idx ? p->cap : 0);
   SVSA_PTR(ws, "ws");
   if (ws_bytes < need) return fail(SVSA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
   int launches = 0;

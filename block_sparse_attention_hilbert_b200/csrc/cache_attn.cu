@@ -48,6 +48,7 @@ static __device__ unsigned int g_cattn_flags;
 
 namespace {
 
+constexpr int kTileRows = 128;              // of the many-row tiles
 constexpr float kShift = 14.f;              // weights are held times 2^kShift
 constexpr int kMinUnits = 8;                // blocks of a CTA at least, where there are as many
 
@@ -61,6 +62,12 @@ struct AttnArgs {
   float* part;                              // [CTA][2][rows][d] sums, then [CTA][2][rows][2] maxima and row sums
   int heads_q, Tq, causal, cap, group, tiles, grid;
   int whole;                                // every item goes to one CTA as a whole
+  // lists gathered per 128-row tile (idx is null then): per item, the blocks
+  // that any of its queries lists, and a bit per query and block
+  const int32_t* ucnt;                      // [items]
+  const int32_t* ulist;                     // [items][max_blocks]
+  const uint32_t* ubits;                    // [items][tile_queries][words]
+  int tile_queries, words;
 };
 
 // A contiguous range of an item's blocks.
@@ -77,8 +84,8 @@ __device__ __forceinline__ int blocks_of(int len) { return max(1, (len + kBlock 
 
 // What the CTAs share out (counts fit 32 bits, checked on the host): blocks, or
 // whole items.  With lists every item counts `cap` blocks, the entries past its
-// own count being empty; without, the items of sequence b have max(1, blocks
-// of b) each.
+// own count being empty; with gathered lists max(1, its union's blocks);
+// without, the items of sequence b have max(1, blocks of b) each.
 struct Shares {
   unsigned total, base, rem;
   int ctas;
@@ -104,6 +111,10 @@ __device__ Shares shares_of(const AttnArgs& p) {
     s.split((unsigned)p.c.B * (p.idx ? p.Tq : 1) * items, p.grid, 1);
   } else if (p.idx) {
     s.split((unsigned)p.c.B * p.Tq * items * p.cap, p.grid, kMinUnits);
+  } else if (p.ucnt) {
+    unsigned n = 0;
+    for (unsigned i = threadIdx.x % 32; i < (unsigned)p.c.B * items; i += 32) n += max(1, __ldg(p.ucnt + i));
+    s.split(__reduce_add_sync(0xffffffffu, n), p.grid, kMinUnits);
   } else {
     unsigned n = 0;
     for (int b = threadIdx.x % 32; b < p.c.B; b += 32) n += blocks_of(seq_len(p, b));
@@ -113,14 +124,19 @@ __device__ Shares shares_of(const AttnArgs& p) {
 }
 
 // The item at unit u: its sequence, head and tile, u's place in it (j0) and
-// its number of units.  `b` and `before` say which sequence u lies in and how
-// many units lie before that (sequences of blocks only).
+// its number of units.  `b` and `before` say which sequence (with gathered
+// lists: which item) u lies in and how many units lie before that (neither
+// with whole items nor with lists).
 __device__ __forceinline__ void item_of(const AttnArgs& p, unsigned u, int b, unsigned before, Segment* s, int* units) {
   unsigned item;
   if (p.whole) {
     item = u;
     s->j0 = 0;
     *units = 1;
+  } else if (p.ucnt) {
+    item = (unsigned)b;
+    s->j0 = (int)(u - before);
+    *units = max(1, __ldg(p.ucnt + b));
   } else {
     const unsigned n = p.idx ? p.cap : blocks_of(seq_len(p, b));
     item = (u - before) / n;
@@ -130,7 +146,7 @@ __device__ __forceinline__ void item_of(const AttnArgs& p, unsigned u, int b, un
   s->t = -1;
   s->tile = (int)(item % p.tiles);
   item /= p.tiles;
-  if (p.whole || p.idx) {
+  if (p.whole || p.idx || p.ucnt) {
     s->h = (int)(item % p.c.heads);
     item /= p.c.heads;
     if (p.idx) {
@@ -144,13 +160,15 @@ __device__ __forceinline__ void item_of(const AttnArgs& p, unsigned u, int b, un
   }
 }
 
-// The sequence of unit u.  A warp calls; 32 sequences a step.
+// The sequence (with gathered lists: the item) of unit u.  A warp calls; 32 a step.
 __device__ void find_sequence(const AttnArgs& p, unsigned u, int* b_out, unsigned* before_out) {
   const int lane = threadIdx.x % 32;
   const unsigned items = (unsigned)p.c.heads * p.tiles;
+  const int n = p.ucnt ? p.c.B * (int)items : p.c.B;
   unsigned before = 0;
-  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-    const unsigned mine = b0 + lane < p.c.B ? blocks_of(seq_len(p, b0 + lane)) * items : 0u;
+  for (int b0 = 0; b0 < n; b0 += 32) {
+    const int b = b0 + lane;
+    const unsigned mine = b >= n ? 0u : p.ucnt ? (unsigned)max(1, __ldg(p.ucnt + b)) : blocks_of(seq_len(p, b)) * items;
     unsigned up = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -717,11 +735,72 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   }
 }
 
+constexpr int kGatherWarps = 32;
+
+// Gathers the lists of one item's queries (a 128-row tile of a key head): a
+// bit per query and block, and the ascending list of the blocks that any of
+// them lists.  A warp per query sets its bits in shared memory; an entry that
+// is not ascending or past the sequence is left out, and recorded.
+__global__ void __launch_bounds__(kGatherWarps * 32)
+cache_gather_kernel(const __grid_constant__ AttnArgs p, int32_t* ucnt, int32_t* ulist, uint32_t* ubits) {
+  extern __shared__ uint32_t rows[];            // [warps][words]
+  __shared__ uint32_t all[1024];
+  __shared__ int warp_tot[kGatherWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  unsigned item = blockIdx.x;
+  const int tile = (int)(item % p.tiles);
+  item /= p.tiles;
+  const int h = (int)(item % p.c.heads), b = (int)(item / p.c.heads);
+  const int t0 = (int)((long long)tile * kTileRows / p.group);
+  const int t1 = (int)min(((long long)(tile + 1) * kTileRows - 1) / p.group, (long long)p.Tq - 1);
+  const int len = seq_len(p, b);
+  for (int i = threadIdx.x; i < p.words; i += blockDim.x) all[i] = 0u;
+  __syncthreads();
+  uint32_t* mine = rows + warp * p.words;
+  for (int t = t0 + warp; t <= t1; t += kGatherWarps) {
+    for (int i = lane; i < p.words; i += 32) mine[i] = 0u;
+    __syncwarp();
+    const long long r = ((long long)b * p.Tq + t) * p.c.heads + h;
+    const int32_t* list = p.idx + r * p.cap;
+    const int n0 = __ldg(p.cnt + r), n = min(max(n0, 0), p.cap);
+    bool bad = n != n0;
+    for (int i = lane; i < n; i += 32) {
+      const int before = i > 0 ? __ldg(list + i - 1) : -1, j = __ldg(list + i);
+      if (j > before && j >= 0 && j < p.c.max_blocks && (long long)j * kBlock < len) atomicOr(&mine[j >> 5], 1u << (j & 31));
+      else bad = true;
+    }
+    if (bad) atomicOr(&g_cattn_flags, kFlagIndex);
+    __syncwarp();
+    uint32_t* out = ubits + ((long long)blockIdx.x * p.tile_queries + (t - t0)) * p.words;
+    for (int i = lane; i < p.words; i += 32) {
+      out[i] = mine[i];
+      if (mine[i]) atomicOr(&all[i], mine[i]);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  // a thread per word (at most 1024): where its blocks go in the list
+  const uint32_t w = threadIdx.x < p.words ? all[threadIdx.x] : 0u;
+  int up = __popc(w);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += v;
+  }
+  if (lane == 31) warp_tot[warp] = up;
+  __syncthreads();
+  int at = up - __popc(w);
+  for (int i = 0; i < warp; ++i) at += warp_tot[i];
+  int32_t* list = ulist + (long long)blockIdx.x * p.c.max_blocks + at;
+  for (uint32_t m = w; m; m &= m - 1) *list++ = (int)threadIdx.x * 32 + __ffs(m) - 1;
+  if (threadIdx.x == blockDim.x - 1) ucnt[blockIdx.x] = at + __popc(w);
+}
+
 #include "cache_attn_rows.cuh"
 
 // Joins the items that several CTAs shared: block (c, y) looks at the item
 // that the start of CTA c + 1's share splits, and if c holds its first unit
-// joins its rows y, y + gridDim.y, ...
+// joins some of its rows.
 template <int D, typename T, int ROWS>
 __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_constant__ AttnArgs p) {
   constexpr int V = D / 4;                      // lanes of four columns
@@ -735,7 +814,7 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
   const unsigned u = sh.first(cta + 1);
   int seq = 0;
   unsigned before = 0;
-  if (!p.idx) find_sequence(p, u, &seq, &before);
+  if (!p.idx) find_sequence(p, u, &seq, &before);      // (a gathered item has no idx)
   Segment s;
   int units;
   item_of(p, u, seq, before, &s, &units);
@@ -746,27 +825,34 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
 
   cudaGridDependencySynchronize();
   const float* stats = p.part + 2LL * p.grid * ROWS * D;
+  auto slot_of = [&](int c, int row) { return (2LL * c + (c == cta ? 1 : 0)) * ROWS + row; };
   const int v = threadIdx.x % V, g = threadIdx.x / V;
-  for (int row = blockIdx.y; row < ROWS; row += gridDim.y) {
+  const bool few = last - cta < 2 * G;          // a lane group per row, else all of them on one
+  for (int base = blockIdx.y * (few ? G : 1); base < ROWS; base += gridDim.y * (few ? G : 1)) {
+    const int row = few ? base + g : base;
     int t, hg;
-    if (!row_of<ROWS>(p, s, row, &t, &hg)) return;            // (rows past the end are the last ones)
-    auto slot_of = [&](int c) { return (2LL * c + (c == cta ? 1 : 0)) * ROWS + row; };
-    float top = -INFINITY;
-    for (int c = cta + (int)threadIdx.x % 32; c <= last; c += 32) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c)));
-    top = warp_max(top);
-    const float z = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
+    const bool live = row_of<ROWS>(p, s, row, &t, &hg);       // (rows past the end are the last ones)
+    if (!few && !live) return;
+    float top = -INFINITY, sum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      for (int c = cta; c <= last; ++c) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c, row)));
+      const float z = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-    for (int c = cta + g; c <= last; c += G) {
-      const long long k = slot_of(c);
-      const float w = tc::ex2(__ldcg(stats + 2 * k) - z);
-      sum += w * __ldcg(stats + 2 * k + 1);
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part + k * D) + v);
-      x.x += w * a.x;
-      x.y += w * a.y;
-      x.z += w * a.z;
-      x.w += w * a.w;
+      for (int c = cta + (few ? 0 : g); c <= last; c += few ? 1 : G) {
+        const long long k = slot_of(c, row);
+        const float w = tc::ex2(__ldcg(stats + 2 * k) - z);
+        sum += w * __ldcg(stats + 2 * k + 1);
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part + k * D) + v);
+        x.x += w * a.x;
+        x.y += w * a.y;
+        x.z += w * a.z;
+        x.w += w * a.w;
+      }
+    }
+    if (few) {
+      if (live) write_out<D, T>(p, s, t, hg, 4 * v, x, top, sum);
+      continue;
     }
     sums[g][v] = x;
     if (v == 0) rowsum[g] = sum;
@@ -828,11 +914,14 @@ cudaError_t run(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& p,
 
 template <int D, typename T, bool I8>
 cudaError_t run_rows(const AttnArgs& p, cudaStream_t st) {
-  constexpr auto kernel = cache_attn_rows_kernel<D, T, I8>;
-  cudaError_t e = allow_smem<kernel>(kRowsSmem);
-  if (e != cudaSuccess) return e;
-  kernel<<<p.grid, kRowsThreads, kRowsSmem, st>>>(p);
-  e = cudaGetLastError();
+  auto go = [&](auto L_) {
+    constexpr auto kernel = cache_attn_rows_kernel<D, T, I8, decltype(L_)::value>;
+    cudaError_t e = allow_smem<kernel>(kRowsSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<p.grid, kRowsThreads, kRowsSmem, st>>>(p);
+    return cudaGetLastError();
+  };
+  const cudaError_t e = p.ucnt ? go(std::true_type{}) : go(std::false_type{});
   return e != cudaSuccess || p.whole ? e : join<D, T, kTileRows>(p, st);
 }
 
@@ -847,10 +936,54 @@ int tile_rows(long long rows, bool lists, int d) {
 
 }  // namespace
 
-size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq) {
-  // (with or without lists: the larger)
-  const int rows = tile_rows((long long)heads_q / c.heads * Tq, false, c.d);
-  return (size_t)kNumSMs * 2 * std::max(rows, 16) * (c.d + 2) * sizeof(float);
+namespace {
+
+// Lists gathered per 128-row tile of queries: the tile visits every block that
+// one of its queries lists, rows masked by a bit per query and block.
+struct Gather {
+  bool use;
+  long long items;
+  int tiles, queries, words;                // queries: of a tile at most (one may lie in two)
+  size_t bits, list, count, total;          // offsets in the workspace, after the partial sums
+};
+Gather gather_plan(const CacheArgs& c, int heads_q, int Tq, int cap) {
+  Gather g{};
+  const long long group = heads_q / c.heads, rows = group * Tq;
+  g.tiles = ceil_div(rows, kTileRows);
+  g.items = (long long)c.B * c.heads * g.tiles;
+  g.queries = (int)std::min<long long>(Tq, (kTileRows - 1) / group + 2);
+  g.words = ceil_div(c.max_blocks, 32);
+  // Per key head: block visits of the lists' own tiles, 0.33 us of an SM each
+  // (0.45 with 16 rows), against those of the gathered tiles, 0.95 us each,
+  // and about 30 us more for their start, gathering and joining (over 148 SMs
+  // and all heads).
+  const long long small = (group + (group <= 8 ? 7 : 15)) / (group <= 8 ? 8 : 16);
+  const double heads = (double)c.B * c.heads;
+  const double lists = heads * Tq * small * std::min(cap, c.max_blocks) * (group <= 8 ? 0.33 : 0.45);
+  const double gathered = heads * g.tiles * c.max_blocks * 0.95 + 30.0 * kNumSMs;
+  g.use = Tq > 1 && c.max_blocks <= 32768 && g.items <= 4096 && gathered < lists;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) & ~(size_t)255; return o; };
+  g.count = take((size_t)g.items * 4);
+  g.list = take((size_t)g.items * c.max_blocks * 4);
+  g.bits = take((size_t)g.items * g.queries * g.words * 4);
+  g.total = g.use ? off : 0;
+  return g;
+}
+
+size_t partial_bytes(int rows, int d) { return ((size_t)kNumSMs * 2 * rows * (d + 2) * sizeof(float) + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq, int cap) {
+  // whole cache, and with cap > 0 lists too: the larger
+  const long long rows = (long long)heads_q / c.heads * Tq;
+  size_t need = partial_bytes(std::max(tile_rows(rows, false, c.d), 16), c.d);
+  if (cap > 0) {
+    const Gather g = gather_plan(c, heads_q, Tq, cap);
+    if (g.use) need = std::max(need, partial_bytes(kTileRows, c.d) + g.total);
+  }
+  return need;
 }
 
 cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, int Tq, int f16, int causal,
@@ -869,21 +1002,38 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   p.causal = causal;
   p.cap = cap;
   p.group = heads_q / c.heads;
-  const long long rows = idx ? p.group : (long long)p.group * Tq;
-  const int tile = tile_rows(rows, idx != nullptr, c.d);
-  p.tiles = ceil_div(rows, tile);
   p.grid = kNumSMs;
+  const Gather g = idx ? gather_plan(c, heads_q, Tq, cap) : Gather{};
+  const long long rows = idx && !g.use ? p.group : (long long)p.group * Tq;
+  const int tile = g.use ? kTileRows : tile_rows(rows, idx != nullptr, c.d);
+  p.tiles = ceil_div(rows, tile);
+  cudaError_t e = cudaSuccess;
+  if (g.use) {
+    char* base = static_cast<char*>(ws) + partial_bytes(kTileRows, c.d);
+    p.ucnt = reinterpret_cast<int32_t*>(base + g.count);
+    p.ulist = reinterpret_cast<int32_t*>(base + g.list);
+    p.ubits = reinterpret_cast<uint32_t*>(base + g.bits);
+    p.tile_queries = g.queries;
+    p.words = g.words;
+    e = allow_smem<cache_gather_kernel>(kGatherWarps * 4096);
+    if (e != cudaSuccess) return e;
+    cache_gather_kernel<<<(unsigned)g.items, kGatherWarps * 32, kGatherWarps * g.words * 4, st>>>(
+        p, reinterpret_cast<int32_t*>(base + g.count), reinterpret_cast<int32_t*>(base + g.list),
+        reinterpret_cast<uint32_t*>(base + g.bits));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    p.idx = p.cnt = idx = nullptr;
+  }
   // Whole items per CTA where no item is longer than two rounds of the warps,
   // or where the items, all alike, fill the CTAs to within 5%: the second
   // kernel takes 3 us, and so does a round trip of the partial sums.
   const long long items = (long long)c.B * (idx ? Tq : 1) * c.heads * p.tiles;
   const long long rounds = (items + kNumSMs - 1) / kNumSMs;
-  p.whole = (idx ? cap : c.max_blocks) <= 16 || (idx && items * 20 >= rounds * kNumSMs * 19);
+  p.whole = !g.use && ((idx ? cap : c.max_blocks) <= 16 || (idx && items * 20 >= rounds * kNumSMs * 19));
   CUtensorMap mk, mv;
   const long long map_rows = (long long)c.n_pages * c.heads * kBlock;
   if (tile <= 16 && (!map_codes(&mk, c.k, map_rows, c.d) || !map_codes(&mv, c.v, map_rows, c.d)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaSuccess;
   auto by_rows = [&](auto D_, auto z, auto i8) {
     constexpr int D = decltype(D_)::value;
     constexpr bool I8 = decltype(i8)::value;
@@ -902,13 +1052,16 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   };
   if (c.d == 128) by_type(std::integral_constant<int, 128>{});
   else by_type(std::integral_constant<int, 64>{});
-  *launches = p.whole ? 1 : 2;
+  *launches = (p.whole ? 1 : 2) + g.use;
   return e;
 }
 
 // Units of one call at most (32-bit counters).
 long long cache_attn_units(const CacheArgs& c, int heads_q, int Tq, const int32_t* idx, int cap) {
-  const long long group = heads_q / c.heads, rows = idx ? group : group * Tq;
+  const long long group = heads_q / c.heads;
+  const Gather g = idx ? gather_plan(c, heads_q, Tq, cap) : Gather{};
+  if (g.use) return g.items * c.max_blocks;
+  const long long rows = idx ? group : group * Tq;
   const int tile = tile_rows(rows, idx != nullptr, c.d);
   return (long long)c.B * (idx ? Tq : 1) * c.heads * ((rows + tile - 1) / tile) * (idx ? cap : c.max_blocks);
 }

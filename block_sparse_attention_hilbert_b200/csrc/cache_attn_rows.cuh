@@ -28,7 +28,6 @@
 // Bound by the hand-offs of a step (widen, S, softmax, P V): without the
 // widening the same loop takes two thirds of the time.
 
-constexpr int kTileRows = 128;
 constexpr int kRowsThreads = 512;               // 16 warps, 128 registers a thread
 constexpr int kWideners = kRowsThreads - 288;   // warps 1-3 and 12 on
 constexpr int kKvStages = 2, kSBufs = 2;        // steps in shared memory, and in S buffers
@@ -71,7 +70,7 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
 // The CTA's segments, in the order that every role walks them.
 struct Segments {
   Shares sh;
-  unsigned u, u_end, before;
+  unsigned u, u_end, before, item;              // item: with gathered lists
   int seq;
   // a warp calls; false: nothing for this CTA
   __device__ bool init(const AttnArgs& p) {
@@ -80,7 +79,7 @@ struct Segments {
     u = sh.first(blockIdx.x);
     u_end = sh.first(blockIdx.x + 1);
     seq = 0;
-    before = 0;
+    before = item = 0;
     if (!p.whole) find_sequence(p, u, &seq, &before);
     return true;
   }
@@ -92,24 +91,32 @@ struct Segments {
     s->j1 = (int)min((unsigned)units, s->j0 + (u_end - u));
     *whole = *starts && s->j1 == units;
     u += s->j1 - s->j0;
-    if (!p.whole && u - before == (unsigned)units * p.c.heads * p.tiles) {
+    if (p.ucnt ? s->j1 == units : !p.whole && u - before == (unsigned)units * p.c.heads * p.tiles) {
       before = u;
       seq += 1;
     }
     *len = seq_len(p, s->b);
     if (p.whole) s->j1 = blocks_of(*len);
+    if (p.ucnt) {                               // (an item without a block has one unit, and nothing in it)
+      item = ((unsigned)s->b * p.c.heads + s->h) * p.tiles + s->tile;
+      if (__ldg(p.ucnt + item) == 0) *len = 0;
+    }
     return true;
   }
 };
 
-// The page of block j, or -1 (an empty sequence, a page out of range).
+// The block of unit j, and its page, or -1 (an empty sequence, a page out of range).
+template <bool LISTS>
+__device__ __forceinline__ int block_of(const AttnArgs& p, unsigned item, int j) {
+  return LISTS ? __ldg(p.ulist + (long long)item * p.c.max_blocks + j) : j;
+}
 __device__ __forceinline__ int page_of(const AttnArgs& p, int b, int j, int len) {
   if (len <= 0) return -1;
   const int page = __ldg(p.c.table + (long long)b * p.c.max_blocks + j);
   return (unsigned)page < (unsigned)p.c.n_pages ? page : -1;
 }
 
-template <int D, typename T, bool I8>
+template <int D, typename T, bool I8, bool LISTS>
 __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const __grid_constant__ AttnArgs p) {
   using namespace tc;
   constexpr int KSTEPS = D / 16;
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       auto step_of = [&](int g) { return g == 0 ? 0 : g & 1 ? min((g + 1) / 2, steps - 1) : g / 2 - 1; };
       auto number = [&](int g, int e) {          // the page of stage g's half e
         const int j = s.j0 + 2 * step_of(g) + e;
-        return g < 2 * steps && j < s.j1 ? page_of(p, s.b, j, len) : -1;
+        return g < 2 * steps && j < s.j1 && len > 0 ? page_of(p, s.b, block_of<LISTS>(p, walk.item, j), len) : -1;
       };
       auto scale = [&](int g, int page) {        // its value scale (1 where there is none to look at)
         return g < 2 * steps && is_v(g) && page >= 0 ? __ldg(p.c.v_scale + (long long)page * p.c.heads + s.h) : 1.f;
@@ -257,10 +264,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int page = e ? p1 : p0;
+            const int blk = page < 0 || !v ? 0 : block_of<LISTS>(p, walk.item, j + e);
             const char* src = static_cast<const char*>(v ? p.c.v : p.c.k) +
                               (size_t)(unsigned)(max(page, 0) * p.c.heads + s.h) * (kBlock * D) + piece;
             const uint32_t to = sbase + kRowsOffRaw + slot * 16384 + e * (kBlock * D) + piece;
-            const int rows = page < 0 ? 0 : v ? min(len - (j + e) * kBlock, kBlock) : kBlock;
+            const int rows = page < 0 ? 0 : v ? min(len - blk * kBlock, kBlock) : kBlock;
 #pragma unroll
             for (int i = 0; i < P; ++i)
               if (r0 + RPP * i < kBlock)
@@ -329,7 +337,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       n += (uint32_t)steps;
       if (len > 0 && ok) {                       // pages out of range, recorded
         bool bad = false;
-        for (int j = s.j0 + t; j < s.j1; j += kWideners) bad = bad || page_of(p, s.b, j, len) < 0;
+        for (int j = s.j0 + t; j < s.j1; j += kWideners)
+          bad = bad || page_of(p, s.b, block_of<LISTS>(p, walk.item, j), len) < 0;
         if (bad) atomicOr(&g_cattn_flags, kFlagIndex);
       }
     }
@@ -400,27 +409,37 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
 
       float ry = 0.f, rs = 0.f, l = 0.f;         // references of y and s (log2), row sum against rs
       bool have = false;
-      // page j's scales and first token, one step ahead
-      auto scales = [&](int j, float* ks, float* vs, int* tok) {
+      // page j's scales and first token, one step ahead; with gathered lists also
+      // whether this row's query lists it (`ahead`: the block, another step ahead)
+      const uint32_t* bits = nullptr;
+      if (LISTS) bits = p.ubits + ((long long)walk.item * p.tile_queries + (live ? t - (int)((long long)s.tile * kTileRows / p.group) : 0)) * p.words;
+      int ahead = s.j0 + half;
+      if (LISTS) ahead = len > 0 && ahead < s.j1 ? block_of<LISTS>(p, walk.item, ahead) : 0;
+      auto scales = [&](int j, float* ks, float* vs, int* tok, uint32_t* listed) {
         *ks = *vs = 0.f;
         *tok = 1 << 30;
-        if (j < s.j1) {
-          const int page = page_of(p, s.b, j, len);
+        *listed = 1u;
+        const int blk = LISTS ? ahead : j;
+        if (LISTS && len > 0 && j + 2 < s.j1) ahead = block_of<LISTS>(p, walk.item, j + 2);
+        if (j < s.j1 && len > 0) {
+          const int page = page_of(p, s.b, blk, len);
+          if (LISTS) *listed = __ldg(bits + (blk >> 5)) >> (blk & 31) & 1u;
           if (page >= 0) {
             const long long cell = (long long)page * p.c.heads + s.h;
             *ks = __ldg(p.c.k_scale + cell);
             *vs = __ldg(p.c.v_scale + cell);
-            *tok = j * kBlock;
+            *tok = blk * kBlock;
           }
         }
       };
       float ks, vs, ks_n, vs_n;
       int tok, tok_n;
-      scales(s.j0 + half, &ks, &vs, &tok);
+      uint32_t listed, listed_n;
+      scales(s.j0 + half, &ks, &vs, &tok, &listed);
       const int steps = max((s.j1 - s.j0 + 1) / 2, 1);      // (a page that is not there is masked)
       for (int i = 0; i < steps; ++i) {
         const uint32_t x = n + (uint32_t)i, sb = x % kSBufs;
-        scales(s.j0 + 2 * (i + 1) + half, &ks_n, &vs_n, &tok_n);
+        scales(s.j0 + 2 * (i + 1) + half, &ks_n, &vs_n, &tok_n, &listed_n);
         if (!__all_sync(0xffffffffu, wait_bar(bar(kBarSFull + sb), (x / kSBufs) & 1u, dead, 111))) {
           stop = true;
           break;
@@ -446,7 +465,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
           m3 = max3(m3, v[c + 6], v[c + 7]);
         }
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-        const float smax = edge ? top : top * f;
+        const bool skip = LISTS && !listed;      // (the row's query does not list this page)
+        const float smax = skip ? -INFINITY : edge ? top : top * f;
         float alpha = 1.f;
         if (smax > -INFINITY) {
           const float ymax = smax + lv;
@@ -487,8 +507,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         }
         // P = 2^(s + lv - ry) as fp16 pairs over the first 32 of this half's 64 S columns
         uint32_t pk[32];
-        const float shift = lv - ry;
+        const float shift = skip ? -INFINITY : lv - ry;
         const F2 ff = edge ? f2(1.f, 1.f) : f2(f, f), zz = f2(shift, shift);
+        // the row sum's terms are 2^gap times the weights; where a tiny value
+        // scale makes that too much for fp32, they are taken on their own
+        const float gap = ry - lv - rs;
+        float lone = 0.f;
+        if (__any_sync(0xffffffffu, gap > 60.f)) {
+          const F2 rr = f2(-rs, -rs);
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float e0, e1;
+            split2(fma2(f2(v[c], v[c + 1]), ff, rr), e0, e1);
+            lone += ex2(e0) + ex2(e1);
+          }
+        }
         F2 sum0 = f2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
@@ -511,11 +544,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         if (lane == 0) mbar_arrive(bar(kBarPFull + half * kSBufs + sb));
         float a0, a1;
         split2(add2(sum0, sum1), a0, a1);
-        // sum of 2^(s - rs)
-        l += (a0 + a1) * ex2(ry - lv - rs);
+        if (!skip) l += gap > 60.f ? lone : (a0 + a1) * ex2(gap);
         ks = ks_n;
         vs = vs_n;
         tok = tok_n;
+        listed = listed_n;
       }
       n += (uint32_t)steps;
 

@@ -861,3 +861,90 @@ def test_many_rows_leave_out_pages_out_of_range():
     o, lse = gpu.attend(q)
     _index_error()
     assert torch.all(o[0] == 0)
+
+
+def test_many_rows_keep_the_weights_of_pages_with_tiny_values():
+    """Pages whose value scales lie 170 and more binary orders below others': they add nothing to the sums but all of
+    their weight to the row sum."""
+    gpu = _filled(1, 1, 64, "e4m3", [640])
+    pages = gpu.table[0, :10].long()
+    gpu.v_scale[pages, 0] = torch.tensor([1e25, 1e-25, 1e-25, 1e25, 1.0, 1e-30, 1e-27, 1.0, 1e25, 1e20], device="cuda")
+    q = torch.randn(1, 1, 70, 64, generator=_gen(27)).to(BF).cuda()
+    o, lse = gpu.attend(q, causal=False)
+    _check_attention(gpu, q, o, lse, False)
+
+
+GATHERED = [
+    # lens, heads, group, Tq, d, dtype, code, cap, the lists' blocks: shared ones and drawn ones
+    ([3840], 2, 1, 200, 128, BF, "e4m3", 40, "drawn"),
+    ([3800], 3, 3, 150, 64, HF, "i8", 40, "drawn"),
+    ([3840], 2, 5, 230, 128, HF, "i8", 40, "near"),
+    ([6000, 100, 0], 1, 1, 200, 64, BF, "e4m3", 60, "near"),
+]
+
+
+@pytest.mark.parametrize("lens,heads,group,Tq,d,dtype,code,cap,kind", GATHERED)
+def test_lists_of_many_queries_match_the_oracle(lens, heads, group, Tq, d, dtype, code, cap, kind):
+    """Enough queries that their lists are gathered per tile: drawn lists, and lists of neighbours that share most of
+    their blocks; empty ones among them."""
+    B = len(lens)
+    gpu = _filled(B, heads, d, code, lens)
+    launches = svsa.svsa_launch_count()
+    rng = np.random.default_rng(4)
+    idx = np.zeros((B, Tq, heads, cap), dtype=np.int32)
+    cnt = np.zeros((B, Tq, heads), dtype=np.int32)
+    for b in range(B):
+        nb = -(-lens[b] // 64)
+        for t in range(Tq):
+            for h in range(heads):
+                if kind == "near":
+                    pool = np.unique(np.clip(t * nb // Tq + np.arange(-8, 9), 0, nb - 1)) if nb else np.zeros(0, int)
+                else:
+                    pool = np.arange(nb)
+                n = int(rng.integers(0, min(cap, len(pool)) + 1))
+                cnt[b, t, h] = n
+                idx[b, t, h, :n] = np.sort(rng.permutation(pool)[:n])
+    idx, cnt = torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda()
+    q = torch.randn(B, heads * group, Tq, d, generator=_gen(28)).to(dtype).cuda()
+    launches = svsa.svsa_launch_count()
+    o, lse = gpu.attend(q, False, idx, cnt)
+    assert svsa.svsa_launch_count() - launches == 3        # gathered: lists, tiles, joining
+    svsa.svsa_sync_status()
+    _check_attention(gpu, q, o, lse, False, _lists(idx, cnt))
+    o, lse = gpu.attend(q, True, idx, cnt)
+    _check_attention(gpu, q, o, lse, True, _lists(idx, cnt))
+    again, _ = gpu.attend(q, True, idx, cnt, lse=False)
+    assert torch.equal(o, again)
+
+
+def test_gathered_lists_leave_out_bad_entries_and_pages():
+    gpu = _filled(1, 2, 128, "i8", [3840])
+    Tq, cap = 200, 40
+    idx = torch.arange(20, 60, dtype=torch.int32, device="cuda").repeat(1, Tq, 2, 1)
+    cnt = torch.full((1, Tq, 2), cap, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 2, Tq, 128, generator=_gen(29)).to(BF).cuda()
+    gpu.attend(q, True, idx, cnt)
+    svsa.svsa_sync_status()
+    idx[0, 7, 0, 5] = 3                                    # not ascending
+    idx[0, 9, 1, 39] = 60                                  # past the sequence
+    cnt[0, 11, 0], cnt[0, 12, 0] = -4, 41
+    o, lse = gpu.attend(q, True, idx, cnt)
+    _index_error()
+    lists = np.empty((1, Tq, 2), dtype=object)
+    for t in range(Tq):
+        for h in range(2):
+            lists[0, t, h] = list(range(20, 60))
+    lists[0, 7, 0].remove(25)                              # (the entry after it ascends again)
+    lists[0, 9, 1].remove(59)
+    lists[0, 11, 0] = []
+    _check_attention(gpu, q, o, lse, True, lists)
+    gpu.table[0, 30] = -1
+    idx[0, 7, 0, 5], idx[0, 9, 1, 39] = 25, 59
+    cnt.fill_(cap)
+    o, lse = gpu.attend(q, True, idx, cnt)
+    _index_error()
+    for t in range(Tq):
+        for h in range(2):
+            lists[0, t, h] = [j for j in range(20, 60) if j != 30]
+    gpu.table[0, 30] = 5
+    _check_attention(gpu, q, o, lse, True, lists)

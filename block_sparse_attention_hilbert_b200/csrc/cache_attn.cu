@@ -836,7 +836,13 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
     float top = -INFINITY, sum = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
-      for (int c = cta; c <= last; ++c) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c, row)));
+      if (few) {
+#pragma unroll 4
+        for (int c = cta; c <= last; ++c) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c, row)));
+      } else {
+        for (int c = cta + (int)threadIdx.x % 32; c <= last; c += 32) top = fmaxf(top, __ldcg(stats + 2 * slot_of(c, row)));
+        top = warp_max(top);
+      }
       const float z = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
       for (int c = cta + (few ? 0 : g); c <= last; c += few ? 1 : G) {
@@ -890,7 +896,7 @@ bool map_codes(CUtensorMap* m, const void* base, long long rows, int d) {
 template <int D, typename T, int ROWS>
 cudaError_t join(const AttnArgs& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.grid, ROWS < 16 ? ROWS : 16);
+  cfg.gridDim = dim3((unsigned)p.grid, ROWS < 32 ? ROWS : 32);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute at[1];

@@ -9,13 +9,15 @@
 // cores, two pages to a step:
 //     S [128 x 128] = Q [128 x d] K^T       (fp16, the codes themselves)
 //     O_h [128 x d] += P_h [128 x 64] V_h   (h = 0, 1: the step's pages; P in tensor memory)
-// Roles: warp 0 issues the MMAs; warps 4-11 are two softmax warpgroups, one
-// thread per query row each, one for each page of a step, with a maximum, a
-// row sum and an accumulator of their own, merged at the item's end; warps
-// 1-3 and 12-15 widen the pages.  Measured on 1560 queries x
-// 12 heads over 32,760 tokens: 694 us with one page to a step, 645 with two,
-// 625 with seven widening warps for three and their loads through shared
-// memory, 554 (567 TFLOP/s) with the next step's K widened before this one's V.
+// Roles: warp 0 issues the MMAs; warp 1 copies the codes; warps 4-11 are two
+// softmax warpgroups, one thread per query row each, one for each page of a
+// step, with a maximum, a row sum and an accumulator of their own, merged at
+// the item's end; warps 2, 3 and 12-15 widen the pages.  Measured on 1560
+// queries x 12 heads over 32,760 tokens: 694 us with one page to a step, 645
+// with two, 554 with the next step's K widened before this one's V, 411 (765
+// TFLOP/s) with the copies and the tables in a warp of their own, which looks
+// 32 blocks up at a time (510 with both in a seventh widening warp, whose
+// time every stage then waits for).
 //
 // Scales: the key scale joins the softmax's factor.  The value scale goes
 // into the weights as an exponent, P = 2^(y - m'), y = s + log2 vs, with a
@@ -25,31 +27,31 @@
 // page's values as zeros.)  Both references are lazy: raised only when passed
 // by 2^12.
 //
-// Bound by the hand-offs of a step (widen, S, softmax, P V): without the
-// widening the same loop takes two thirds of the time.
+// Bound by the hand-offs of a step (S, softmax, P V): without the widening the
+// same loop takes nine tenths of the time.
 
 constexpr int kRowsThreads = 512;               // 16 warps, 128 registers a thread
-constexpr int kWideners = kRowsThreads - 288;   // warps 1-3 and 12 on
-constexpr int kKvStages = 2, kSBufs = 2;        // steps in shared memory, and in S buffers
+constexpr int kWideWarps = 6;                   // warps 2, 3 and 12-15
+constexpr int kKvStages = 3, kSBufs = 2;        // stages (a step's K or V) in shared memory, steps in S buffers
 constexpr float kLazy = 12.f;
 constexpr float kLeastScale = 1.17549435e-38f;  // a value scale below the normal range counts as zero
 constexpr uint32_t kStep = 32768;               // 128 keys x 128 columns of fp16
-constexpr uint32_t kRowsOffK = kStep, kRowsOffV = kRowsOffK + kKvStages * kStep;
-constexpr uint32_t kRowsOffRaw = kRowsOffV + kKvStages * kStep;
-constexpr int kRaw = 3;                         // stages of codes in flight
+constexpr uint32_t kRowsOffKv = kStep, kRowsOffRaw = kRowsOffKv + kKvStages * kStep;
+constexpr int kRaw = 5;                         // stages of codes in flight
 constexpr uint32_t kRowsOffMisc = kRowsOffRaw + kRaw * 16384;
 constexpr int kRowsSmem = (int)kRowsOffMisc + 4096 + 1024;      // + alignment of the tiles
 constexpr uint32_t kColO = 256;                 // S buffers at 0 and 128; accumulators at 256, 256 + d
 
 enum : int {
-  kBarQFull = 0, kBarQEmpty, kBarKFull, kBarKEmpty = kBarKFull + kKvStages, kBarVFull = kBarKEmpty + kKvStages,
-  kBarVEmpty = kBarVFull + kKvStages, kBarSFull = kBarVEmpty + kKvStages,
+  kBarQFull = 0, kBarQEmpty, kBarKvFull, kBarKvEmpty = kBarKvFull + kKvStages, kBarSFull = kBarKvEmpty + kKvStages,
   kBarPFull = kBarSFull + kSBufs,               // [2 halves][kSBufs]
   kBarSFree = kBarPFull + 2 * kSBufs, kBarOFull = kBarSFree + kSBufs, kBarOEmpty, kBarEnd, kBars
 };
 
 struct RowsMisc {
   uint64_t bar[kBars];
+  uint64_t raw_full[kRaw], raw_empty[kRaw];     // the stages of codes
+  int2 rows[kRaw];                              // rows of their two pages
   uint32_t tmem, abort;
   float fac[kTileRows];
   float xch[2][3][kTileRows];                   // of each half: reference of y, of s, row sum
@@ -116,6 +118,13 @@ __device__ __forceinline__ int page_of(const AttnArgs& p, int b, int j, int len)
   return (unsigned)page < (unsigned)p.c.n_pages ? page : -1;
 }
 
+// A segment's stages: K 0, K 1, V 0, K 2, V 1, ..., V steps - 1.
+__device__ __forceinline__ int stages_of(const Segment& s) { return (s.j1 - s.j0 + 1) / 2 * 2; }
+__device__ __forceinline__ bool is_v(int g, int stages) { return g > 0 && ((g & 1) == 0 || g == stages - 1); }
+__device__ __forceinline__ int step_of(int g, int stages) {
+  return g == 0 ? 0 : g & 1 ? min((g + 1) / 2, stages / 2 - 1) : g / 2 - 1;
+}
+
 template <int D, typename T, bool I8, bool LISTS>
 __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const __grid_constant__ AttnArgs p) {
   using namespace tc;
@@ -135,16 +144,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
     mbar_init(bar(kBarQFull), 1);
     mbar_init(bar(kBarQEmpty), 1);
     for (int i = 0; i < kKvStages; ++i) {
-      mbar_init(bar(kBarKFull + i), kWideners / 32);
-      mbar_init(bar(kBarKEmpty + i), 1);
-      mbar_init(bar(kBarVFull + i), kWideners / 32);
-      mbar_init(bar(kBarVEmpty + i), 1);
+      mbar_init(bar(kBarKvFull + i), kWideWarps);
+      mbar_init(bar(kBarKvEmpty + i), 1);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(bar(kBarSFull + i), 1);
       mbar_init(bar(kBarPFull + i), 4);          // the first warpgroup
       mbar_init(bar(kBarPFull + kSBufs + i), 4);
       mbar_init(bar(kBarSFree + i), 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(su32(&ms->raw_full[i]), 1);
+      mbar_init(su32(&ms->raw_empty[i]), kWideWarps);
     }
     mbar_init(bar(kBarOFull), 1);
     mbar_init(bar(kBarOEmpty), 8);
@@ -174,18 +185,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       constexpr uint32_t ID_S = idesc_f16(false, false, false, 128, 128);   // Q . K^T
       constexpr uint32_t ID_O = idesc_f16(false, false, true, D, 128);      // P . V, V MN-major
       const uint64_t dQ = sdesc(sbase, 16, 1024);
-      const uint64_t dK = sdesc(sbase + kRowsOffK, 16, 1024);
-      const uint64_t dV = sdesc(sbase + kRowsOffV, 16384, 1024);
-      uint32_t n = 0, item = 0;                 // steps before this item; items
+      const uint64_t dK = sdesc(sbase + kRowsOffKv, 16, 1024);
+      const uint64_t dV = sdesc(sbase + kRowsOffKv, 16384, 1024);
+      uint32_t n = 0, item = 0;                 // steps before this item (two stages each); items
       bool ok = true;
       while (ok && walk.next(p, &s, &len, &starts, &whole)) {
         ok = wait_bar(bar(kBarQFull), item & 1u, dead, 101);
-        const uint32_t first = n, end = n + (uint32_t)max((s.j1 - s.j0 + 1) / 2, 1);
+        const uint32_t first = n, end = n + (uint32_t)stages_of(s) / 2;
         // S runs one step ahead of P V
         for (uint32_t x = first; ok && x <= end; ++x) {
           if (x < end) {
-            const uint32_t st = x % kKvStages, sb = x % kSBufs;
-            ok = wait_bar(bar(kBarKFull + st), (x / kKvStages) & 1u, dead, 102) &&
+            const uint32_t g = x == first ? 2 * x : 2 * x - 1, st = g % kKvStages, sb = x % kSBufs;
+            ok = wait_bar(bar(kBarKvFull + st), (g / kKvStages) & 1u, dead, 102) &&
                  wait_bar(bar(kBarSFree + sb), ((x / kSBufs) & 1u) ^ 1u, dead, 103);
             if (!ok) break;
             tc_fence_after();
@@ -195,13 +206,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
               const uint32_t off = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
               umma_f16(tmem + sb * 128, dQ + off, b0 + off, ID_S, kk > 0 ? 1u : 0u);
             }
-            umma_commit(bar(kBarKEmpty + st));
+            umma_commit(bar(kBarKvEmpty + st));
             umma_commit(bar(kBarSFull + sb));
             if (x == end - 1) umma_commit(bar(kBarQEmpty));
           }
           if (x > first) {
-            const uint32_t y = x - 1, st = y % kKvStages, sb = y % kSBufs;
-            ok = wait_bar(bar(kBarVFull + st), (y / kKvStages) & 1u, dead, 104) &&
+            const uint32_t y = x - 1, g = x == end ? 2 * y + 1 : 2 * y + 2, st = g % kKvStages, sb = y % kSBufs;
+            ok = wait_bar(bar(kBarKvFull + st), (g / kKvStages) & 1u, dead, 104) &&
                  (y > first || wait_bar(bar(kBarOEmpty), (item & 1u) ^ 1u, dead, 105));
             const uint64_t b0 = dV + ((st * kStep) >> 4);
 #pragma unroll
@@ -215,7 +226,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
                             ID_O, (y > first || kk > 0) ? 1u : 0u);
             }
             if (!ok) break;
-            umma_commit(bar(kBarVEmpty + st));
+            umma_commit(bar(kBarKvEmpty + st));
             umma_commit(bar(kBarSFree + sb));
           }
         }
@@ -231,116 +242,123 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
   } else if (warp < 4 || warp >= 12) {
     // ---------------------------------------------------------------- widening
     // Stages of two pages' K or V, in the order in which they are needed: K of
-    // the next step before V of this one (V is read a softmax later).  Thread t
-    // takes the 16-byte pieces (r0 + RPP i, cc) of each page, laid over the
-    // lanes so that the fp16 stores (swizzled) meet no bank twice.  It copies
-    // them to a ring of kRaw stages in shared memory ahead of time and reads
-    // back its own bytes only, so the ring needs no barrier.
+    // the next step before V of this one (V is read a softmax later).  One warp
+    // copies the codes to a ring of kRaw stages ahead of time, a bulk copy to a
+    // page; six widen them, warp w rows RW w + RPP i of the stage's 128.  The
+    // 16-byte pieces lie over the lanes so that neither the loads of codes nor
+    // the fp16 stores (swizzled) meet a bank twice.
     constexpr int CPR = D / 16;                  // pieces of a row of codes
-    constexpr int RPP = kWideners / CPR;         // rows per pass
-    constexpr int P = (kBlock + RPP - 1) / RPP;
-    const int t = warp < 4 ? tid - 32 : tid - 288;
-    const int cc = D == 128 ? (t & 3) | (t >> 1 & 4) : t & 3;
-    const int r0 = D == 128 ? (t >> 2 & 1) | (t >> 3 & 2) | (t >> 5 << 2) : t >> 2;
-    const int piece = (r0 * CPR + cc) * 16;
-    uint32_t n = 0;
+    constexpr int RW = 32 / CPR;                 // rows of a pass
+    constexpr int RPP = RW * kWideWarps;
+    constexpr int P = (2 * kBlock + RPP - 1) / RPP;
+    const int ww = warp < 4 ? warp - 2 : warp - 10;      // (-1: the copying warp)
+    const int cc = lane & (CPR - 1);
+    const int r0 = ww * RW + (D == 128 ? (lane >> 3 & 2) | ((lane >> 2 ^ lane >> 3) & 1) : lane >> 2);
+    uint32_t n = 0, asked = 0;                   // stages before this item; copied by now
     bool ok = true;
     while (ok && walk.next(p, &s, &len, &starts, &whole)) {
-      const int steps = (s.j1 - s.j0 + 1) / 2;   // (a page that is not there is zeros)
-      // stage g: K 0, K 1, V 0, K 2, V 1, ..., V steps - 1
-      auto is_v = [&](int g) { return g > 0 && ((g & 1) == 0 || g == 2 * steps - 1); };
-      auto step_of = [&](int g) { return g == 0 ? 0 : g & 1 ? min((g + 1) / 2, steps - 1) : g / 2 - 1; };
-      auto number = [&](int g, int e) {          // the page of stage g's half e
-        const int j = s.j0 + 2 * step_of(g) + e;
-        return g < 2 * steps && j < s.j1 && len > 0 ? page_of(p, s.b, block_of<LISTS>(p, walk.item, j), len) : -1;
-      };
-      auto scale = [&](int g, int page) {        // its value scale (1 where there is none to look at)
-        return g < 2 * steps && is_v(g) && page >= 0 ? __ldg(p.c.v_scale + (long long)page * p.c.heads + s.h) : 1.f;
-      };
-      // stage g, of the pages p0 and p1 (-1: zeros), into the ring's place `slot`; V rows past the sequence: zeros
-      auto ask = [&](int g, int p0, int p1, uint32_t slot) {
-        if (g < 2 * steps) {
-          const int v = is_v(g), j = s.j0 + 2 * step_of(g);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int page = e ? p1 : p0;
-            const int blk = page < 0 || !v ? 0 : block_of<LISTS>(p, walk.item, j + e);
-            const char* src = static_cast<const char*>(v ? p.c.v : p.c.k) +
-                              (size_t)(unsigned)(max(page, 0) * p.c.heads + s.h) * (kBlock * D) + piece;
-            const uint32_t to = sbase + kRowsOffRaw + slot * 16384 + e * (kBlock * D) + piece;
-            const int rows = page < 0 ? 0 : v ? min(len - blk * kBlock, kBlock) : kBlock;
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-              if (r0 + RPP * i < kBlock)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to + i * RPP * D), "l"(src + i * RPP * D),
-                             "r"(r0 + RPP * i < rows ? 16 : 0) : "memory");
-          }
+      const int stages = stages_of(s);           // (a page that is not there is zeros)
+      // The copying warp looks blocks up 32 at a time, one to a lane, two batches
+      // at hand: the tables' latency is met once in 16 steps.
+      int blks[2], pages[2];
+      float scales[2];
+      auto look = [&](int batch, int* blk, int* page, float* scale) {
+        const int j = s.j0 + 32 * batch + lane;
+        *blk = 0;
+        *page = -1;
+        *scale = 0.f;
+        if (j < s.j1 && len > 0) {
+          *blk = block_of<LISTS>(p, walk.item, j);
+          *page = page_of(p, s.b, *blk, len);
+          if (*page >= 0) *scale = __ldg(p.c.v_scale + (long long)*page * p.c.heads + s.h);
         }
-        asm volatile("cp.async.commit_group;\n" ::: "memory");
       };
-      float z[kRaw][2];
-      uint32_t slot = 0;
-#pragma unroll
-      for (int i = 0; i < kRaw; ++i) {
-        const int p0 = number(i, 0), p1 = number(i, 1);
-        z[i][0] = scale(i, p0);
-        z[i][1] = scale(i, p1);
-        ask(i, p0, p1, i);
+      // starts the copies of stage g and says how many rows of each page there are
+      // (V rows past the sequence, and those of a value scale of zero, are zeros)
+      auto ask = [&](int g) {
+        const uint32_t to = asked % kRaw;
+        if (!__all_sync(0xffffffffu, wait_bar(su32(&ms->raw_empty[to]), ((asked / kRaw) & 1u) ^ 1u, dead, 114))) return false;
+        const bool v = is_v(g, stages);
+        const int j = 2 * step_of(g, stages), from = (j & 31) + (lane & 1);
+        const bool odd = j >> 5 & 1;
+        const int blk = __shfl_sync(0xffffffffu, odd ? blks[1] : blks[0], from);
+        const int page = __shfl_sync(0xffffffffu, odd ? pages[1] : pages[0], from);
+        const float scale = __shfl_sync(0xffffffffu, odd ? scales[1] : scales[0], from);
+        int rows = 0;
+        if (page >= 0) rows = !v ? kBlock : scale >= kLeastScale ? min(max(len - blk * kBlock, 0), kBlock) : 0;
+        const int other = __shfl_sync(0xffffffffu, rows, 1);
+        const uint32_t full = su32(&ms->raw_full[to]);
+        if (lane == 0) {
+          ms->rows[to] = make_int2(rows, other);
+          mbar_expect_tx(full, (uint32_t)(rows + other) * D);
+        }
+        __syncwarp();
+        if (rows && lane < 2)
+          bulk_load(sbase + kRowsOffRaw + to * 16384 + lane * (kBlock * D),
+                    static_cast<const char*>(v ? p.c.v : p.c.k) + ((long long)page * p.c.heads + s.h) * (kBlock * D), (uint32_t)rows * D,
+                    full);
+        ++asked;
+        // the values of a batch's first step are the last to need the batch before
+        if (v && (j & 31) == 0) {
+          if (odd) look((j >> 5) + 1, &blks[0], &pages[0], &scales[0]);
+          else look((j >> 5) + 1, &blks[1], &pages[1], &scales[1]);
+        }
+        return true;
+      };
+      if (ww < 0) {
+        look(0, &blks[0], &pages[0], &scales[0]);
+        for (int g = 0; ok && g < stages; ++g) ok = ask(g);
+        n += (uint32_t)stages;
+        continue;
       }
-      int p0 = number(kRaw, 0), p1 = number(kRaw, 1);
-      for (int g = 0; g < 2 * steps; ++g) {
-        const int v = is_v(g);
-        const uint32_t x = n + (uint32_t)step_of(g), st = x % kKvStages;
-        asm volatile("cp.async.wait_group %0;\n" ::"n"(kRaw - 1) : "memory");
-        ok = wait_bar(bar((v ? kBarVEmpty : kBarKEmpty) + st), ((x / kKvStages) & 1u) ^ 1u, dead, 108 + v);
+      for (int g = 0; g < stages; ++g) {
+        const int v = is_v(g, stages);
+        const uint32_t x = n + (uint32_t)g, st = x % kKvStages, from_st = x % kRaw;
+        ok = ok && wait_bar(su32(&ms->raw_full[from_st]), (x / kRaw) & 1u, dead, 115) &&
+             wait_bar(bar(kBarKvEmpty + st), ((x / kKvStages) & 1u) ^ 1u, dead, 108);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        const uint32_t from = sbase + kRowsOffRaw + from_st * 16384 + r0 * D + cc * 16;
+        const uint32_t to = sbase + kRowsOffKv + st * kStep + (uint32_t)(cc >> 2) * 16384 + r0 * 128;
+        const int2 rows = ms->rows[from_st];
+        const bool full = rows.x + rows.y == 2 * kBlock;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool none = !(z[0][e] >= kLeastScale);      // (a value scale of zero: zeros)
-          const uint32_t from = sbase + kRowsOffRaw + slot * 16384 + e * (kBlock * D) + piece;
-          const uint32_t to = sbase + (v ? kRowsOffV : kRowsOffK) + st * kStep + (uint32_t)(cc >> 2) * 16384 + e * 8192 + r0 * 128;
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const int r = r0 + RPP * i;
-            if (r < kBlock) {
-              uint4 c = lds128(from + i * RPP * D);
-              if (none) c = make_uint4(0u, 0u, 0u, 0u);
-              uint32_t y[8];
-              Widen<I8>::word(c.x, y[0], y[1]);
-              Widen<I8>::word(c.y, y[2], y[3]);
-              Widen<I8>::word(c.z, y[4], y[5]);
-              Widen<I8>::word(c.w, y[6], y[7]);
-              const uint32_t at = to + RPP * i * 128 + ((((cc & 3) * 2) ^ (r & 7)) << 4);
-              st_shared_v4(at, y[0], y[1], y[2], y[3]);
-              st_shared_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
+        for (int i = 0; i < P; ++i) {
+          if (ww * RW + RPP * i < 2 * kBlock) {
+            uint4 c = lds128(from + i * RPP * D);
+            if (!full) {
+              const int r = r0 + RPP * i;
+              if (r >= kBlock ? r - kBlock >= rows.y : r >= rows.x) c = make_uint4(0u, 0u, 0u, 0u);
             }
+            uint32_t y[8];
+            Widen<I8>::word(c.x, y[0], y[1]);
+            Widen<I8>::word(c.y, y[2], y[3]);
+            Widen<I8>::word(c.z, y[4], y[5]);
+            Widen<I8>::word(c.w, y[6], y[7]);
+            const uint32_t at = to + i * RPP * 128 + ((((cc & 3) * 2) ^ ((r0 + RPP * i) & 7)) << 4);
+            st_shared_v4(at, y[0], y[1], y[2], y[3]);
+            st_shared_v4(at ^ 16u, y[4], y[5], y[6], y[7]);
           }
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar((v ? kBarVFull : kBarKFull) + st));
-        // the stage kRaw further on takes this one's place (its pages' numbers were read a stage ago)
-#pragma unroll
-        for (int i = 0; i + 1 < kRaw; ++i) {
-          z[i][0] = z[i + 1][0];
-          z[i][1] = z[i + 1][1];
+        if (lane == 0) {
+          mbar_arrive(bar(kBarKvFull + st));
+          mbar_arrive(su32(&ms->raw_empty[from_st]));
         }
-        z[kRaw - 1][0] = scale(g + kRaw, p0);
-        z[kRaw - 1][1] = scale(g + kRaw, p1);
-        ask(g + kRaw, p0, p1, slot);
-        p0 = number(g + kRaw + 1, 0);
-        p1 = number(g + kRaw + 1, 1);
-        slot = slot + 1 == kRaw ? 0 : slot + 1;
       }
-      asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-      n += (uint32_t)steps;
+      n += (uint32_t)stages;
       if (len > 0 && ok) {                       // pages out of range, recorded
         bool bad = false;
-        for (int j = s.j0 + t; j < s.j1; j += kWideners)
+        for (int j = s.j0 + ww * 32 + lane; j < s.j1; j += kWideWarps * 32)
           bad = bad || page_of(p, s.b, block_of<LISTS>(p, walk.item, j), len) < 0;
         if (bad) atomicOr(&g_cattn_flags, kFlagIndex);
       }
+    }
+    if (ww < 0) {                                // the copies in flight, before the CTA goes
+      volatile uint32_t no_abort = 0u;
+      for (uint32_t x = asked > kRaw ? asked - kRaw : 0u; x < asked; ++x)
+        wait_bar(su32(&ms->raw_full[x % kRaw]), (x / kRaw) & 1u, &no_abort, 116);
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -409,37 +427,42 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
 
       float ry = 0.f, rs = 0.f, l = 0.f;         // references of y and s (log2), row sum against rs
       bool have = false;
-      // page j's scales and first token, one step ahead; with gathered lists also
-      // whether this row's query lists it (`ahead`: the block, another step ahead)
-      const uint32_t* bits = nullptr;
-      if (LISTS) bits = p.ubits + ((long long)walk.item * p.tile_queries + (live ? t - (int)((long long)s.tile * kTileRows / p.group) : 0)) * p.words;
-      int ahead = s.j0 + half;
-      if (LISTS) ahead = len > 0 && ahead < s.j1 ? block_of<LISTS>(p, walk.item, ahead) : 0;
-      auto scales = [&](int j, float* ks, float* vs, int* tok, uint32_t* listed) {
+      // this half's pages, looked up 32 steps at a time, one to a lane, and the
+      // next 32 half way through them: block (-1: not there) and scales
+      auto look = [&](int i, int* blk, float* ks, float* vs) {
+        const int j = s.j0 + 2 * (i + lane) + half;
+        *blk = -1;
         *ks = *vs = 0.f;
-        *tok = 1 << 30;
-        *listed = 1u;
-        const int blk = LISTS ? ahead : j;
-        if (LISTS && len > 0 && j + 2 < s.j1) ahead = block_of<LISTS>(p, walk.item, j + 2);
         if (j < s.j1 && len > 0) {
-          const int page = page_of(p, s.b, blk, len);
-          if (LISTS) *listed = __ldg(bits + (blk >> 5)) >> (blk & 31) & 1u;
+          const int b = block_of<LISTS>(p, walk.item, j), page = page_of(p, s.b, b, len);
           if (page >= 0) {
             const long long cell = (long long)page * p.c.heads + s.h;
+            *blk = b;
             *ks = __ldg(p.c.k_scale + cell);
             *vs = __ldg(p.c.v_scale + cell);
-            *tok = blk * kBlock;
           }
         }
       };
-      float ks, vs, ks_n, vs_n;
-      int tok, tok_n;
-      uint32_t listed, listed_n;
-      scales(s.j0 + half, &ks, &vs, &tok, &listed);
-      const int steps = max((s.j1 - s.j0 + 1) / 2, 1);      // (a page that is not there is masked)
+      int blk_c, blk_n = -1;
+      float ks_c, vs_c, ks_n = 0.f, vs_n = 0.f;
+      look(0, &blk_c, &ks_c, &vs_c);
+      // with gathered lists, whether this row's query lists the page, a step ahead
+      const uint32_t* bits = nullptr;
+      if (LISTS) bits = p.ubits + ((long long)walk.item * p.tile_queries + (live ? t - (int)((long long)s.tile * kTileRows / p.group) : 0)) * p.words;
+      auto lists = [&](int blk) { return !LISTS || blk < 0 || (__ldg(bits + (blk >> 5)) >> (blk & 31) & 1u); };
+      bool listed = lists(__shfl_sync(0xffffffffu, blk_c, 0)), listed_n = listed;
+      const int steps = stages_of(s) / 2;        // (a page that is not there is masked)
       for (int i = 0; i < steps; ++i) {
         const uint32_t x = n + (uint32_t)i, sb = x % kSBufs;
-        scales(s.j0 + 2 * (i + 1) + half, &ks_n, &vs_n, &tok_n, &listed_n);
+        if ((i & 31) == 16) look(i + 16, &blk_n, &ks_n, &vs_n);
+        const int blk = __shfl_sync(0xffffffffu, blk_c, i & 31), tok = blk < 0 ? 1 << 30 : blk * kBlock;
+        const float ks = __shfl_sync(0xffffffffu, ks_c, i & 31), vs = __shfl_sync(0xffffffffu, vs_c, i & 31);
+        if ((i & 31) == 31) {
+          blk_c = blk_n;
+          ks_c = ks_n;
+          vs_c = vs_n;
+        }
+        if (LISTS) listed_n = lists(__shfl_sync(0xffffffffu, blk_c, (i + 1) & 31));
         if (!__all_sync(0xffffffffu, wait_bar(bar(kBarSFull + sb), (x / kSBufs) & 1u, dead, 111))) {
           stop = true;
           break;
@@ -545,9 +568,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         float a0, a1;
         split2(add2(sum0, sum1), a0, a1);
         if (!skip) l += gap > 60.f ? lone : (a0 + a1) * ex2(gap);
-        ks = ks_n;
-        vs = vs_n;
-        tok = tok_n;
         listed = listed_n;
       }
       n += (uint32_t)steps;

@@ -933,11 +933,17 @@ cudaError_t run_rows(const AttnArgs& p, cudaStream_t st) {
 
 // Rows of a tile for this many query rows per key head (or per list).  16-row
 // tiles widen the codes again for each, 128-row tiles cost the same for one
-// row as for 128.  32 rows over 4 caches of 60-65k tokens, d = 128: two 16-row
-// tiles 189 us, one of 128 rows 218 us, so three 16-row tiles would lose; d =
-// 64: 112 and 176 us, so four would.
-int tile_rows(long long rows, bool lists, int d) {
-  return rows <= 8 ? 8 : lists || rows <= (d == 128 ? 32 : 48) ? 16 : kTileRows;
+// row as for 128 and start later.  A visit of a page takes an SM 0.43 us
+// per 16-row tile (d = 64: 0.23) and 0.72 us (0.62) on 128 rows, which pay 6 to 9 us
+// more to start: 32 rows over 4 caches of 60-65k tokens 188 us in two tiles
+// and 168 on 128 rows, over 2 of 2-3k tokens 20 and 25; d = 64, 48 rows: 156 and
+// 148, and 17 and 22.  The lengths are on the device, so the caches' room counts.
+int tile_rows(long long rows, bool lists, const CacheArgs& c) {
+  if (rows <= 8) return 8;
+  if (lists || rows <= 16) return 16;
+  if (rows > (c.d == 128 ? 32 : 48)) return kTileRows;
+  const double more = ceil_div(rows, 16) * (c.d == 128 ? 0.43 : 0.23) - (c.d == 128 ? 0.72 : 0.62);
+  return more * c.B * c.heads * c.max_blocks > 10.0 * kNumSMs ? kTileRows : 16;
 }
 
 }  // namespace
@@ -960,13 +966,13 @@ Gather gather_plan(const CacheArgs& c, int heads_q, int Tq, int cap) {
   g.queries = (int)std::min<long long>(Tq, (kTileRows - 1) / group + 2);
   g.words = ceil_div(c.max_blocks, 32);
   // Per key head: block visits of the lists' own tiles, 0.33 us of an SM each
-  // (0.45 with 16 rows), against those of the gathered tiles, 0.95 us each,
+  // (0.45 with 16 rows), against those of the gathered tiles, 0.72 us each,
   // and about 30 us more for their start, gathering and joining (over 148 SMs
   // and all heads).
   const long long small = (group + (group <= 8 ? 7 : 15)) / (group <= 8 ? 8 : 16);
   const double heads = (double)c.B * c.heads;
   const double lists = heads * Tq * small * std::min(cap, c.max_blocks) * (group <= 8 ? 0.33 : 0.45);
-  const double gathered = heads * g.tiles * c.max_blocks * 0.95 + 30.0 * kNumSMs;
+  const double gathered = heads * g.tiles * c.max_blocks * 0.72 + 30.0 * kNumSMs;
   g.use = Tq > 1 && c.max_blocks <= 32768 && g.items <= 4096 && gathered < lists;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t o = off; off += (bytes + 255) & ~(size_t)255; return o; };
@@ -984,7 +990,7 @@ size_t partial_bytes(int rows, int d) { return ((size_t)kNumSMs * 2 * rows * (d 
 size_t cache_attn_workspace_bytes(const CacheArgs& c, int heads_q, int Tq, int cap) {
   // whole cache, and with cap > 0 lists too: the larger
   const long long rows = (long long)heads_q / c.heads * Tq;
-  size_t need = partial_bytes(std::max(tile_rows(rows, false, c.d), 16), c.d);
+  size_t need = partial_bytes(std::max(tile_rows(rows, false, c), 16), c.d);
   if (cap > 0) {
     const Gather g = gather_plan(c, heads_q, Tq, cap);
     if (g.use) need = std::max(need, partial_bytes(kTileRows, c.d) + g.total);
@@ -1011,7 +1017,7 @@ cudaError_t launch_cache_attn(const CacheArgs& c, const void* q, int heads_q, in
   p.grid = kNumSMs;
   const Gather g = idx ? gather_plan(c, heads_q, Tq, cap) : Gather{};
   const long long rows = idx && !g.use ? p.group : (long long)p.group * Tq;
-  const int tile = g.use ? kTileRows : tile_rows(rows, idx != nullptr, c.d);
+  const int tile = g.use ? kTileRows : tile_rows(rows, idx != nullptr, c);
   p.tiles = ceil_div(rows, tile);
   cudaError_t e = cudaSuccess;
   if (g.use) {
@@ -1068,7 +1074,7 @@ long long cache_attn_units(const CacheArgs& c, int heads_q, int Tq, const int32_
   const Gather g = idx ? gather_plan(c, heads_q, Tq, cap) : Gather{};
   if (g.use) return g.items * c.max_blocks;
   const long long rows = idx ? group : group * Tq;
-  const int tile = tile_rows(rows, idx != nullptr, c.d);
+  const int tile = tile_rows(rows, idx != nullptr, c);
   return (long long)c.B * (idx ? Tq : 1) * c.heads * ((rows + tile - 1) / tile) * (idx ? cap : c.max_blocks);
 }
 

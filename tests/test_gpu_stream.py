@@ -817,6 +817,15 @@ def test_attention_of_many_rows_matches_the_oracle(lens, heads, group, Tq, d, dt
     assert torch.equal(o, again)
 
 
+@pytest.mark.parametrize("heads,group,Tq,d,blocks", [(4, 4, 5, 128, 1400), (4, 8, 4, 128, 1400), (4, 4, 12, 64, 2700), (2, 2, 12, 64, 40)])
+def test_rows_of_few_tiles_in_caches_of_any_room(heads, group, Tq, d, blocks):
+    gpu = _filled(2, heads, d, "e4m3", [1500, 70], blocks=blocks)
+    q = torch.randn(2, heads * group, Tq, d, generator=_gen(26)).to(BF).cuda()
+    o, lse = gpu.attend(q, True)
+    svsa.svsa_sync_status()
+    _check_attention(gpu, q, o, lse, True)
+
+
 def test_many_rows_with_scales_of_any_size_and_rows_that_are_not_finite():
     gpu = _filled(1, 1, 128, "i8", [1280])
     pages = gpu.table[0, :20].long()

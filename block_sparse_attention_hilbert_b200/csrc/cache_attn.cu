@@ -810,7 +810,12 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
   // (everything up to the wait reads only what was there before the first kernel)
   const Shares sh = shares_of(p);
   const int cta = blockIdx.x;
-  if (cta + 1 >= sh.ctas) return;
+  // A block without an item to join leaves; the first one waits all the same,
+  // so that this grid does not end before the kernel it joins.
+  auto leave = [&]() {
+    if ((blockIdx.x | blockIdx.y) == 0) cudaGridDependencySynchronize();
+  };
+  if (cta + 1 >= sh.ctas) return leave();
   const unsigned u = sh.first(cta + 1);
   int seq = 0;
   unsigned before = 0;
@@ -818,9 +823,9 @@ __global__ void __launch_bounds__(128) cache_attn_join_kernel(const __grid_const
   Segment s;
   int units;
   item_of(p, u, seq, before, &s, &units);
-  if (s.j0 == 0) return;                        // the share begins with an item
+  if (s.j0 == 0) return leave();                // the share begins with an item
   const unsigned u0 = u - s.j0;
-  if (sh.of(u0) != cta) return;                 // an earlier CTA holds the item's first unit
+  if (sh.of(u0) != cta) return leave();         // an earlier CTA holds the item's first unit
   const int last = sh.of(u0 + units - 1);
 
   cudaGridDependencySynchronize();

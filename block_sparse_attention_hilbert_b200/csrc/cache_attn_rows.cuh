@@ -14,7 +14,7 @@
 // step, with a maximum, a row sum and an accumulator of their own, merged at
 // the item's end; warps 2, 3 and 12-15 widen the pages.  Measured on 1560
 // queries x 12 heads over 32,760 tokens: 694 us with one page to a step, 645
-// with two, 554 with the next step's K widened before this one's V, 411 (765
+// with two, 554 with the next step's K widened before this one's V, 408 (771
 // TFLOP/s) with the copies and the tables in a warp of their own, which looks
 // 32 blocks up at a time (510 with both in a seventh widening warp, whose
 // time every stage then waits for).
@@ -322,19 +322,25 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         const uint32_t to = sbase + kRowsOffKv + st * kStep + (uint32_t)(cc >> 2) * 16384 + r0 * 128;
         const int2 rows = ms->rows[from_st];
         const bool full = rows.x + rows.y == 2 * kBlock;
+        uint4 c[P];                              // all loads before the first store
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          if (ww * RW + RPP * i < 2 * kBlock) c[i] = lds128(from + i * RPP * D);
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int r = r0 + RPP * i;
+            if (r >= kBlock ? r - kBlock >= rows.y : r >= rows.x) c[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           if (ww * RW + RPP * i < 2 * kBlock) {
-            uint4 c = lds128(from + i * RPP * D);
-            if (!full) {
-              const int r = r0 + RPP * i;
-              if (r >= kBlock ? r - kBlock >= rows.y : r >= rows.x) c = make_uint4(0u, 0u, 0u, 0u);
-            }
             uint32_t y[8];
-            Widen<I8>::word(c.x, y[0], y[1]);
-            Widen<I8>::word(c.y, y[2], y[3]);
-            Widen<I8>::word(c.z, y[4], y[5]);
-            Widen<I8>::word(c.w, y[6], y[7]);
+            Widen<I8>::word(c[i].x, y[0], y[1]);
+            Widen<I8>::word(c[i].y, y[2], y[3]);
+            Widen<I8>::word(c[i].z, y[4], y[5]);
+            Widen<I8>::word(c[i].w, y[6], y[7]);
             const uint32_t at = to + i * RPP * 128 + ((((cc & 3) * 2) ^ ((r0 + RPP * i) & 7)) << 4);
             st_shared_v4(at, y[0], y[1], y[2], y[3]);
             st_shared_v4(at ^ 16u, y[4], y[5], y[6], y[7]);

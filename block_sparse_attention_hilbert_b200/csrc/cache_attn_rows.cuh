@@ -23,9 +23,10 @@
 // into the weights as an exponent, P = 2^(y - m'), y = s + log2 vs, with a
 // reference m' of its own for y, so the fp16 weights are measured against the
 // largest contribution to the output whatever the scales; the row sum is
-// kept against the maximum of s.  (A scale of zero counts as one, and the
-// page's values as zeros.)  Both references are lazy: raised only when passed
-// by 2^12.
+// kept against the maximum of s.  A page whose value scale is zero (or below
+// the normal range) has no part in the output: its weights are zeros, it does
+// not touch m', and its terms of the row sum are taken on their own.  Both
+// references are lazy: raised only when passed by 2^12.
 //
 // Bound by the hand-offs of a step (S, softmax, P V): without the widening the
 // same loop takes nine tenths of the time.
@@ -35,6 +36,7 @@ constexpr int kWideWarps = 6;                   // warps 2, 3 and 12-15
 constexpr int kKvStages = 3, kSBufs = 2;        // stages (a step's K or V) in shared memory, steps in S buffers
 constexpr float kLazy = 12.f;
 constexpr float kLeastScale = 1.17549435e-38f;  // a value scale below the normal range counts as zero
+constexpr float kNone = -3e38f;                 // the reference of y before the first page with values
 constexpr uint32_t kStep = 32768;               // 128 keys x 128 columns of fp16
 constexpr uint32_t kRowsOffKv = kStep, kRowsOffRaw = kRowsOffKv + kKvStages * kStep;
 constexpr int kRaw = 5;                         // stages of codes in flight
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       const bool live = row_of<kTileRows>(p, s, row, &t, &hg);
       const int lim = live && p.causal ? max(len - p.Tq + 1 + t, 0) : len;
 
-      float ry = 0.f, rs = 0.f, l = 0.f;         // references of y and s (log2), row sum against rs
+      float ry = kNone, rs = 0.f, l = 0.f;       // references of y and s (log2), row sum against rs
       bool have = false;
       // this half's pages, looked up 32 steps at a time, one to a lane, and the
       // next 32 half way through them: block (-1: not there) and scales
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         tmem_ld32(tmem + lane_off + sb * 128 + 64 * half, v);
         tmem_ld32(tmem + lane_off + sb * 128 + 64 * half + 32, v + 32);
         tmem_wait_ld();
-        const float f = fac * ks, lv = vs >= kLeastScale ? __log2f(vs) : 0.f;
+        const float f = fac * ks, lv = vs >= kLeastScale ? __log2f(vs) : -INFINITY;
         // the largest s of the row (log2 units; f >= 0)
         const bool edge = !__all_sync(0xffffffffu, tok + kBlock <= lim);
         if (edge) {
@@ -498,20 +500,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         const float smax = skip ? -INFINITY : edge ? top : top * f;
         float alpha = 1.f;
         if (smax > -INFINITY) {
-          const float ymax = smax + lv;
-          if (!have) {
+          const float ymax = smax + lv;          // (-inf without values)
+          if (ymax > ry + kLazy) {
+            if (ry != kNone) alpha = ex2(ry - ymax);      // (else the accumulator holds zeros)
             ry = ymax;
+          }
+          if (!have) {
             rs = smax;
             have = true;
-          } else {
-            if (ymax > ry + kLazy) {
-              alpha = ex2(ry - ymax);
-              ry = ymax;
-            }
-            if (smax > rs + kLazy) {
-              l *= ex2(rs - smax);
-              rs = smax;
-            }
+          } else if (smax > rs + kLazy) {
+            l *= ex2(rs - smax);
+            rs = smax;
           }
         }
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -539,7 +538,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         const float shift = skip ? -INFINITY : lv - ry;
         const F2 ff = edge ? f2(1.f, 1.f) : f2(f, f), zz = f2(shift, shift);
         // the row sum's terms are 2^gap times the weights; where a tiny value
-        // scale makes that too much for fp32, they are taken on their own
+        // scale makes that too much for fp32, or there are no values (gap is
+        // infinite), they are taken on their own
         const float gap = ry - lv - rs;
         float lone = 0.f;
         if (__any_sync(0xffffffffu, gap > 60.f)) {

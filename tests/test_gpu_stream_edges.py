@@ -1,0 +1,115 @@
+"""Streaming entry points at the edges of their definitions, on the GPU against 64 bits.
+
+Tolerances of the attention, counted before the first run (u = the output type's half step, finfo.eps / 2), with p_t the
+softmax weights under their largest and S their sum:
+  * (2^-11 + 2^-12) W, W = sum p |v| / S, and u |o|, as in test_gpu_stream.py, but no absolute term: bf16 outputs have
+    none, so outputs of any size are held to the same relative error.
+  * weights below fp16's normal range are off by at most half its smallest step, 2^-25, of what a weight of 1 stands for.
+    The few-row tiles hold p times 2^14: sum 2^-39 |v| / S.  The 128-row tiles hold p times the page's value scale times
+    2^11 or more against the largest such product Y: sum 2^-36 Y |code| / S.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_hilbert_b200 as svsa
+from oracle import stream
+from test_gpu_stream import BF, HF, GpuCache, _filled, _gen, _half, _index_error, _np, _tokens
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    svsa.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    yield
+    svsa.svsa_sync_status()
+
+
+def _check(gpu, q, o, lse, causal, lists=None, many=True):
+    """o and lse against 64 bits, element by element."""
+    ref, qn, got, got_l = gpu.oracle(), _np(q), _np(o), _np(lse)
+    B, hq, Tq, d = qn.shape
+    g = hq // gpu.heads
+    for b in range(B):
+        n = int(ref.len[b])
+        see = np.arange(n)[None] < np.array([stream.visible(n, Tq, t, causal) for t in range(Tq)])[:, None]
+        pages = ref.table[b, :-(-n // 64)]
+        for h in range(gpu.heads):
+            k, v = ref.tokens(b, h)
+            vs = np.repeat(ref.v_scale[pages, h], 64)[:n, None]
+            code = np.abs(v) / np.where(vs > 0, vs, 1.0)
+            mask = see.copy()
+            if lists is not None:
+                for t in range(Tq):
+                    mine = np.zeros(len(pages), dtype=bool)
+                    mine[lists[b, t, h]] = True
+                    mask[t] &= np.repeat(mine, 64)[:n]
+            for e in range(h * g, h * g + g):
+                s = np.where(mask, qn[b, e] @ k.T / math.sqrt(d), -np.inf)
+                empty = ~mask.any(-1)
+                top = np.where(empty, 0.0, s.max(-1, initial=-np.inf))[:, None]
+                p = np.exp(s - top)
+                total = np.where(empty, 1.0, p.sum(-1))[:, None]
+                want, W = p @ v / total, p @ np.abs(v) / total
+                if many:
+                    low = 2.0**-36 * (p * vs[:, 0]).max(-1, initial=0.0)[:, None] * (mask @ code) / total
+                else:
+                    low = 2.0**-39 * (mask @ np.abs(v)) / total
+                tol = (2.0**-11 + 2.0**-12) * W + _half(q.dtype) * np.abs(want) * (1 + 2**-7) + low
+                if q.dtype == HF:
+                    tol = tol + 2.0**-25                     # half of fp16's smallest step
+                err = np.abs(got[b, e] - want)
+                assert np.all(err <= tol), (b, e, float((err / np.maximum(tol, 1e-300)).max()))
+                rl = np.where(empty, -np.inf, top[:, 0] + np.log(np.where(empty, 1.0, p.sum(-1))))
+                assert np.array_equal(np.isinf(got_l[b, e]), empty) and np.all(got_l[b, e][empty] == -np.inf)
+                fin = ~empty
+                assert np.all(np.abs(got_l[b, e][fin] - rl[fin]) <= 2.0**-13 + 2.0**-20 * np.abs(rl[fin]))
+
+
+# ---- blocks of zero values ----------------------------------------------------------------
+
+@pytest.mark.parametrize("code", ["e4m3", "i8"])
+@pytest.mark.parametrize("size", [1.0, 1e-3, 1e-5, 1e-9])
+@pytest.mark.parametrize("gathered", [False, True])
+def test_blocks_of_zero_values_beside_small_ones(size, code, gathered):
+    """A block whose values are all zero has the value scale 0: it adds to the row sums alone, however small the other
+    blocks' values are."""
+    n, d, heads, Tq = (3840, 128, 2, 200) if gathered else (1270, 128, 1, 60)
+    gpu = GpuCache(1, heads, d, code, -(-n // 64), seed=1)
+    k, v = _tokens(_gen(101), 1, heads, n, d, BF)
+    v = v * size
+    for j in (0, 1, 7, 12):
+        v[:, :, 64 * j:64 * j + 64] = 0
+    gpu.append(k, v)
+    assert torch.count_nonzero(gpu.v_scale[gpu.table[0].long()] == 0) == 4 * heads
+    q = torch.randn(1, heads, Tq, d, generator=_gen(41)).to(BF).cuda()
+    if not gathered:
+        for causal in (True, False):
+            o, lse = gpu.attend(q, causal)
+            svsa.svsa_sync_status()
+            _check(gpu, q, o, lse, causal)
+        return
+    rng = np.random.default_rng(5)
+    lists = np.empty((1, Tq, heads), dtype=object)
+    idx, cnt = np.zeros((1, Tq, heads, 40), dtype=np.int32), np.zeros((1, Tq, heads), dtype=np.int32)
+    for t in range(Tq):
+        for h in range(heads):
+            m = int(rng.integers(0, 41))
+            pick = {0, 1, 7} if t == 3 else set(rng.permutation(60)[:m].tolist()) | ({0, 12} if m < 38 else set())
+            lists[0, t, h] = sorted(pick)
+            cnt[0, t, h] = len(pick)
+            idx[0, t, h, :len(pick)] = lists[0, t, h]
+    launches = svsa.svsa_launch_count()
+    o, lse = gpu.attend(q, False, torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda())
+    assert svsa.svsa_launch_count() - launches == 3        # gathered
+    svsa.svsa_sync_status()
+    _check(gpu, q, o, lse, False, lists)

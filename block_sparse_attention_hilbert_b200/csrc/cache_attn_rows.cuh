@@ -26,7 +26,10 @@
 // kept against the maximum of s.  A page whose value scale is zero (or below
 // the normal range) has no part in the output: its weights are zeros, it does
 // not touch m', and its terms of the row sum are taken on their own.  Both
-// references are lazy: raised only when passed by 2^12.
+// references are lazy.  That of s is raised when passed by 2^12.  m' is put
+// 2^11 below the largest y and raised when a y passes it by 2^15 (fp16 ends at
+// 2^16), so that weights down to 2^-36 of the largest keep a value and those
+// down to 2^-25 all of fp16's bits: a tail below one dominant key counts.
 //
 // Bound by the hand-offs of a step (S, softmax, P V): without the widening the
 // same loop takes nine tenths of the time.
@@ -35,8 +38,9 @@ constexpr int kRowsThreads = 512;               // 16 warps, 128 registers a thr
 constexpr int kWideWarps = 6;                   // warps 2, 3 and 12-15
 constexpr int kKvStages = 3, kSBufs = 2;        // stages (a step's K or V) in shared memory, steps in S buffers
 constexpr float kLazy = 12.f;
+constexpr float kHead = 11.f, kRoom = 15.f;     // the largest weights lie between 2^kHead and 2^kRoom
 constexpr float kLeastScale = 1.17549435e-38f;  // a value scale below the normal range counts as zero
-constexpr float kNone = -3e38f;                 // the reference of y before the first page with values
+constexpr float kNone = -3e38f;                 // a reference before the first key
 constexpr uint32_t kStep = 32768;               // 128 keys x 128 columns of fp16
 constexpr uint32_t kRowsOffKv = kStep, kRowsOffRaw = kRowsOffKv + kKvStages * kStep;
 constexpr int kRaw = 5;                         // stages of codes in flight
@@ -433,8 +437,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       const bool live = row_of<kTileRows>(p, s, row, &t, &hg);
       const int lim = live && p.causal ? max(len - p.Tq + 1 + t, 0) : len;
 
-      float ry = kNone, rs = 0.f, l = 0.f;       // references of y and s (log2), row sum against rs
-      bool have = false;
+      float ry = kNone, rs = kNone, l = 0.f;     // references of y and s (log2), row sum against rs
       // this half's pages, looked up 32 steps at a time, one to a lane, and the
       // next 32 half way through them: block (-1: not there) and scales
       auto look = [&](int i, int* blk, float* ks, float* vs) {
@@ -501,15 +504,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         float alpha = 1.f;
         if (smax > -INFINITY) {
           const float ymax = smax + lv;          // (-inf without values)
-          if (ymax > ry + kLazy) {
-            if (ry != kNone) alpha = ex2(ry - ymax);      // (else the accumulator holds zeros)
-            ry = ymax;
+          if (ymax > ry + kRoom) {
+            if (ry != kNone) alpha = ex2(ry - ymax + kHead);      // (else the accumulator holds zeros)
+            ry = ymax - kHead;
           }
-          if (!have) {
-            rs = smax;
-            have = true;
-          } else if (smax > rs + kLazy) {
-            l *= ex2(rs - smax);
+          if (smax > rs + kLazy) {
+            l *= ex2(rs - smax);                 // (of the first key: 0 times 0)
             rs = smax;
           }
         }

@@ -113,3 +113,25 @@ def test_blocks_of_zero_values_beside_small_ones(size, code, gathered):
     assert svsa.svsa_launch_count() - launches == 3        # gathered
     svsa.svsa_sync_status()
     _check(gpu, q, o, lse, False, lists)
+
+
+# ---- a dominant key without a value ---------------------------------------------------------
+
+@pytest.mark.parametrize("code,dtype", [("e4m3", BF), ("i8", HF)])
+@pytest.mark.parametrize("logit", [10.0, 15.0, 17.5, 20.0])
+@pytest.mark.parametrize("Tq", [1, 4, 50])
+def test_the_tail_below_a_dominant_key_without_a_value(logit, Tq, code, dtype):
+    """One key takes nearly all of the weight and its value is zero, so the output is what the others add."""
+    n, d, heads = 2600, 128, 2
+    gpu = GpuCache(1, heads, d, code, -(-n // 64) + 1, seed=2)
+    k, v = _tokens(_gen(102), 1, heads, n, d, BF, scale=0.25)
+    u = torch.randn(d, generator=_gen(42)).sign().to(BF).cuda()
+    for at in (0, 64 * 6 + 3):                              # in a page of either parity
+        k[0, at // 64 % 2, at], v[0, at // 64 % 2, at] = u, 0
+    k[0, 1, 5], v[0, 1, 5] = u, 0
+    gpu.append(k, v * 4)
+    q = (u * (logit / math.sqrt(d)) + 0.1 * torch.randn(1, 3 * heads, Tq, d, generator=_gen(43)).cuda()).to(dtype)
+    o, lse = gpu.attend(q, False)
+    svsa.svsa_sync_status()
+    assert logit - 1 < float(lse.min()) and float(lse.max()) < logit + 9
+    _check(gpu, q, o, lse, False, many=3 * Tq > 48)

@@ -260,7 +260,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 // Query fragments of one row.  The products sum over d in any order, so the k
 // index of the MMA is laid over d as the reads of K want it: lane c of a quad
 // owns the d / 4 consecutive values from c * d / 4 on, four per step.  Returns
-// the power of two that the row was divided by.
+// the power of two that the row was divided by.  A row that is not finite is
+// NaN throughout: so are its scores, but not the masked ones, and a row that
+// sees nothing stays a row that sees nothing.
 template <int D, typename T>
 __device__ __forceinline__ float load_q(const T* q, bool live, int c, uint32_t lo[D / 16], uint32_t hi[D / 16]) {
   float amax = 0.f;
@@ -290,11 +292,10 @@ __device__ __forceinline__ float load_q(const T* q, bool live, int c, uint32_t l
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) {
     const float2 f0 = pair(2 * i), f1 = pair(2 * i + 1);
-    lo[i] = h2bits(__floats2half2_rn(f0.x * down, f0.y * down));
-    hi[i] = h2bits(__floats2half2_rn(f1.x * down, f1.y * down));
+    lo[i] = odd ? 0x7fff7fffu : h2bits(__floats2half2_rn(f0.x * down, f0.y * down));
+    hi[i] = odd ? 0x7fff7fffu : h2bits(__floats2half2_rn(f1.x * down, f1.y * down));
   }
-  const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-  return odd ? __int_as_float(0x7fffffff) : up;           // a row that is not finite gives NaN
+  return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 // A warp's blocks of the segment, up to 32 at a time: lane i holds the page

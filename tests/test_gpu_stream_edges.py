@@ -135,3 +135,48 @@ def test_the_tail_below_a_dominant_key_without_a_value(logit, Tq, code, dtype):
     svsa.svsa_sync_status()
     assert logit - 1 < float(lse.min()) and float(lse.max()) < logit + 9
     _check(gpu, q, o, lse, False, many=3 * Tq > 48)
+
+
+# ---- rows that see nothing --------------------------------------------------------------------
+
+@pytest.mark.parametrize("Tq", [4, 60])
+@pytest.mark.parametrize("d,dtype,code", [(128, BF, "e4m3"), (64, HF, "i8")])
+def test_rows_that_see_nothing_give_zeros_whatever_their_values(Tq, d, dtype, code):
+    """Queries before the first key, and lists without a visible key: zeros and -inf, for rows that are not finite too."""
+    gpu = _filled(2, 1, d, code, [2, 0], dtype=dtype, blocks=3)
+    q = torch.randn(2, 2, Tq, d, generator=_gen(44)).to(dtype).cuda()
+    q[:, 0, 0, 3], q[:, 1, 1, 9], q[:, :, -1, 0] = float("nan"), float("inf"), float("-inf")
+    o, lse = gpu.attend(q, True)
+    svsa.svsa_sync_status()
+    assert torch.all(o[:, :, :-2] == 0) and torch.all(lse[:, :, :-2] == -math.inf)
+    assert torch.all(o[1] == 0) and torch.all(lse[1] == -math.inf)
+    assert torch.isfinite(o[0, :, -2].float()).all() and torch.isnan(o[0, :, -1]).all() and torch.isnan(lse[0, :, -1]).all()
+    # lists: empty, or of blocks that the query does not see yet
+    gpu = _filled(1, 1, d, code, [66], dtype=dtype, blocks=2)
+    q = q[:1, :, -4:].contiguous()
+    q[0, :, 0, 1] = q[0, :, 1, 1] = float("nan")
+    idx = torch.tensor([[0], [1], [1], [0]], dtype=torch.int32, device="cuda").view(1, 4, 1, 1)
+    cnt = torch.tensor([0, 1, 1, 1], dtype=torch.int32, device="cuda").view(1, 4, 1)
+    o, lse = gpu.attend(q, True, idx, cnt)
+    svsa.svsa_sync_status()
+    assert torch.all(o[:, :, :2] == 0) and torch.all(lse[:, :, :2] == -math.inf)
+    assert torch.isfinite(o[:, :, 2].float()).all() and torch.isnan(o[:, :, 3]).all()
+
+
+def test_gathered_rows_that_are_not_finite():
+    """Many queries' lists, gathered: a row without a listed key gives zeros, a row that is not finite NaN, and neither
+    touches its neighbours."""
+    gpu = _filled(1, 2, 128, "e4m3", [3840])
+    Tq, cap = 200, 40
+    idx = torch.arange(20, 60, dtype=torch.int32, device="cuda").repeat(1, Tq, 2, 1)
+    cnt = torch.full((1, Tq, 2), cap, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 2, Tq, 128, generator=_gen(48)).to(BF).cuda()
+    cnt[0, 11, 0] = 0
+    want, want_l = gpu.attend(q, True, idx, cnt)
+    q[0, 0, 11, 5], q[0, 1, 12, 6] = float("inf"), float("nan")
+    o, lse = gpu.attend(q, True, idx, cnt)
+    svsa.svsa_sync_status()
+    assert torch.all(o[0, 0, 11] == 0) and lse[0, 0, 11] == -math.inf
+    assert torch.isnan(o[0, 1, 12]).all() and torch.isnan(lse[0, 1, 12])
+    o[0, 1, 12], lse[0, 1, 12] = want[0, 1, 12], want_l[0, 1, 12]
+    assert torch.equal(o, want) and torch.equal(lse, want_l)

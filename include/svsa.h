@@ -610,11 +610,12 @@ svsa_status svsa_cache_select(const svsa_cache* c, const void* q, int32_t* idx, 
  *   o[b, h, t, :] = sum_n softmax_n(q . k_n / sqrt(d)) v_n
  * over the keys that the query sees, or (idx, cnt given, as svsa_cache_select
  * writes them) over those of them in the query's listed blocks.  A list is
- * strictly ascending; an entry that is not, or that lies past the sequence, is
- * left out and reported (SVSA_ERR_INDEX).  A query that sees no key gives
- * zeros and lse = -inf, whatever its values; one that sees some gives NaN if a
- * value of it is not finite.
- * Rows of the pages past len may hold anything.  o like q; lse nullable fp32
+ * strictly ascending; an entry not above the one before it, or past the
+ * sequence, is left out and reported (SVSA_ERR_INDEX; how often a block counts
+ * that such a list names again further on is not defined).  A query that sees
+ * no key gives zeros and lse = -inf, whatever its values; one that sees some
+ * gives NaN if a value of it is not finite.  Rows of the pages past len may
+ * hold anything.  o like q; lse nullable fp32
  * [B, heads_q, Tq], natural log.  Softmax weights are rounded to fp16 (as in
  * svsa_attn_fwd), statistics and sums are fp32; the result does not depend on
  * the state of the GPU: the same call gives the same bits.  ws:

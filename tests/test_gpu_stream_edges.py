@@ -180,3 +180,23 @@ def test_gathered_rows_that_are_not_finite():
     assert torch.isnan(o[0, 1, 12]).all() and torch.isnan(lse[0, 1, 12])
     o[0, 1, 12], lse[0, 1, 12] = want[0, 1, 12], want_l[0, 1, 12]
     assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
+# ---- lists that name a block twice ------------------------------------------------------------
+
+@pytest.mark.parametrize("Tq", [2, 200])
+def test_a_list_that_comes_back_to_a_block_is_reported_and_touches_no_other(Tq):
+    """[5, 3, 5]: the call is reported, whichever tiles it takes, and the other queries' results are what they were."""
+    gpu = _filled(1, 2, 64, "i8", [3840])
+    cap = 40
+    idx = torch.arange(20, 60, dtype=torch.int32, device="cuda").repeat(1, Tq, 2, 1)
+    cnt = torch.full((1, Tq, 2), cap, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 2, Tq, 64, generator=_gen(45)).to(BF).cuda()
+    want, want_l = gpu.attend(q, True, idx, cnt)
+    svsa.svsa_sync_status()
+    idx[0, 1, 0, :3] = torch.tensor([25, 23, 25], dtype=torch.int32)
+    o, lse = gpu.attend(q, True, idx, cnt)
+    _index_error()
+    assert torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
+    o[0, 0, 1], lse[0, 0, 1] = want[0, 0, 1], want_l[0, 0, 1]
+    assert torch.equal(o, want) and torch.equal(lse, want_l)

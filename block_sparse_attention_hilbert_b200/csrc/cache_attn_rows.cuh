@@ -483,7 +483,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         tmem_ld32(tmem + lane_off + sb * 128 + 64 * half, v);
         tmem_ld32(tmem + lane_off + sb * 128 + 64 * half + 32, v + 32);
         tmem_wait_ld();
-        const float f = fac * ks, lv = vs >= kLeastScale ? __log2f(vs) : -INFINITY;
+        // (a page that is not there has no key either, and no row sum to take on its own)
+        const float f = fac * ks, lv = vs >= kLeastScale ? __log2f(vs) : blk < 0 ? 0.f : -INFINITY;
         // the largest s of the row (log2 units; f >= 0)
         const bool edge = !__all_sync(0xffffffffu, tok + kBlock <= lim);
         if (edge) {

@@ -10,10 +10,15 @@
     o = cache.attend(q, idx, cnt)                         # ... and attend to those
 
 Each call is the entry point of the same purpose in include/svsa.h on the
-current stream; nothing is copied to the host, so a step captured into a CUDA
-graph stays valid while the cache grows.
+current stream, or on `stream`; nothing is copied to the host, so a step
+captured into a CUDA graph stays valid while the cache grows.  A call on
+`stream` does all its work there, workspaces and allocations included, as under
+torch.cuda.stream(stream): it does not wait for the current stream, nor the
+current stream for it.
 """
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -38,6 +43,24 @@ def grid_positions(T: int, H: int, W: int, frame: int = 0, device="cuda"):
     return torch.stack([v.reshape(-1) for v in torch.meshgrid(*axes, indexing="ij")], -1).to(torch.int32).unsqueeze(0).to(device)
 
 
+@contextlib.contextmanager
+def _on(stream, device):
+    """Makes `stream` the current one: what is allocated inside belongs to it, so a workspace that a call drops goes to
+    no other stream while the call still runs.  The call's outputs are also marked (`keep`) as used by the stream that
+    was current, where the caller will use them."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    caller = torch.cuda.current_stream(device)
+
+    def keep(*tensors):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(caller)
+
+    with torch.cuda.stream(stream):
+        yield keep
+
+
 class NormRope:
     """Per-head RMS norm and position rotation of queries and keys (svsa_qk_norm_rope), with its weights and tables."""
 
@@ -59,18 +82,29 @@ class NormRope:
     def __call__(self, q, k, pos=None, *, perm=None, out=None, stream=None):
         """q [B, heads_q, N, d], k [B, heads_k, N, d] or None: views with a contiguous last dimension.  perm int32 [rows]:
         token of each output row (-1: zeros).  Returns (yq, yk) [B, heads, rows, d], into `out` if given."""
+        if stream is not None:
+            with _on(stream, q.device) as keep:
+                y = self(q, k, pos, perm=perm, out=out)
+                if out is None:
+                    keep(*y)
+                return y
         rows = q.shape[2] if perm is None else perm.shape[0]
         if out is None:
             out = tuple(None if x is None else torch.empty((x.shape[0], x.shape[1], rows, x.shape[3]), dtype=x.dtype, device=x.device)
                         for x in (q, k))
         svsa_qk_norm_rope(q, k, self.wq, self.wk if k is not None else None, self.cos, self.sin, pos, perm, *out,
-                          self.params(q, k, pos, rows), stream)
+                          self.params(q, k, pos, rows))
         return out
 
     def backward(self, gq, gk, q, k, pos=None, *, iperm=None, rows=None, out=None, stream=None):
         """Gradients of a call with these inputs: (dq, dk, dwq, dwk).  iperm int32 [N]: the output row of each token and
         `rows` their number, where the call had a perm.  dq, dk go into `out` if given (views of any strides); dwq, dwk
         are fp32 [d]."""
+        if stream is not None:
+            with _on(stream, q.device) as keep:
+                dx = self.backward(gq, gk, q, k, pos, iperm=iperm, rows=rows, out=out)
+                keep(*(dx if out is None else dx[2:]))
+                return dx
         p = self.params(q, k, pos, rows)
         if out is None:
             out = tuple(None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
@@ -78,7 +112,7 @@ class NormRope:
         ws = torch.empty(svsa_qk_norm_rope_bwd_workspace_bytes(p), dtype=torch.uint8, device=q.device)
         dwk = dw[1] if k is not None else None
         svsa_qk_norm_rope_bwd(gq, gk, q, k, self.wq, self.wk if k is not None else None, self.cos, self.sin, pos, iperm,
-                              *out, dw[0], dwk, p, ws, ws.numel(), stream)
+                              *out, dw[0], dwk, p, ws, ws.numel())
         return (*out, dw[0], dwk)
 
 
@@ -110,29 +144,46 @@ class BlockCache:
         self._next = torch.zeros_like(self.length)
         self.cache = block_cache(self.k, self.v, self.k_scale, self.v_scale, self.table, self.length, self.mean, self.mean_scale)
 
-    def append(self, k, v, n_new=None):
+    def append(self, k, v, n_new=None, *, stream=None):
         """k, v [B, heads, N, d] (views with a contiguous last dimension); n_new int32 [B]: how many of the N are real.
-        The lengths are updated on the current stream."""
+        The lengths are updated on the same stream."""
+        if stream is not None:
+            with _on(stream, k.device):
+                return self.append(k, v, n_new)
         svsa_cache_append(self.cache, k, v, n_new, self._next, cache_tokens(k, v))
         self.length.copy_(self._next)
 
     def select(self, q, cap: int, *, first: int = 1, last: int = 1, causal: bool = True, stream=None):
         """Blocks for each query and key head: (idx [B, Tq, heads, cap] ascending, cnt [B, Tq, heads])."""
+        if stream is not None:
+            with _on(stream, q.device) as keep:
+                lists = self.select(q, cap, first=first, last=last, causal=causal)
+                keep(*lists)
+                return lists
         c = self.cache
         idx = torch.empty((c.B, q.shape[2], c.heads, cap), dtype=torch.int32, device=q.device)
         cnt = torch.empty((c.B, q.shape[2], c.heads), dtype=torch.int32, device=q.device)
-        svsa_cache_select(c, q, idx, cnt, cache_query(q, causal=causal, cap=cap, first=first, last=last), stream)
+        svsa_cache_select(c, q, idx, cnt, cache_query(q, causal=causal, cap=cap, first=first, last=last))
         return idx, cnt
 
     def attend(self, q, idx=None, cnt=None, *, causal: bool = True, out=None, lse=None, stream=None):
         """Attention of q [B, heads_q, Tq, d] over the cache, or over each query's listed blocks."""
+        if stream is not None:
+            with _on(stream, q.device) as keep:
+                o = self.attend(q, idx, cnt, causal=causal, out=out, lse=lse)
+                if out is None:
+                    keep(o)
+                return o
         p = cache_query(q, causal=causal, cap=0 if idx is None else idx.shape[-1])
         if out is None:
             out = torch.empty_like(q)
         ws = torch.empty(svsa_cache_attn_workspace_bytes(self.cache, p), dtype=torch.uint8, device=q.device)
-        svsa_cache_attn(self.cache, q, idx, cnt, out, lse, p, ws, ws.numel(), stream)
+        svsa_cache_attn(self.cache, q, idx, cnt, out, lse, p, ws, ws.numel())
         return out
 
-    def reset(self):
-        """Empty every sequence (on the current stream); the pages keep what they hold until written again."""
+    def reset(self, *, stream=None):
+        """Empty every sequence; the pages keep what they hold until written again."""
+        if stream is not None:
+            with _on(stream, self.length.device):
+                return self.reset()
         self.length.zero_()

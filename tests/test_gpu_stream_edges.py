@@ -200,3 +200,71 @@ def test_a_list_that_comes_back_to_a_block_is_reported_and_touches_no_other(Tq):
     assert torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
     o[0, 0, 1], lse[0, 0, 1] = want[0, 0, 1], want_l[0, 0, 1]
     assert torch.equal(o, want) and torch.equal(lse, want_l)
+
+
+# ---- the layers on streams -------------------------------------------------------------------------
+
+def test_layer_calls_in_flight_on_two_streams():
+    """attend, with and without lists, select and gradients queued on two side streams behind some work, while the current
+    stream asks for memory of the same sizes and writes it: each gives what it gives alone."""
+    B, heads, d, n = 2, 4, 128, 9000
+    cache = svsa.BlockCache(B, heads, d, n)
+    k, v = _tokens(_gen(60), B, heads, n, d, BF)
+    cache.append(k, v, torch.tensor([n, 1234], dtype=torch.int32, device="cuda"))
+    rope = svsa.NormRope(d, pairs=(64,), rows=64, wq=torch.linspace(0.5, 1.5, d).cuda())
+    pos = torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40, 1)
+    q = [torch.randn(B, 4 * heads, t, d, generator=_gen(61 + t)).to(BF).cuda() for t in (1, 1, 40, 40)]
+
+    def both(i, s):
+        x = q[i]
+        idx, cnt = cache.select(x, 9, stream=s)
+        out = [idx, cnt, cache.attend(x, stream=s), cache.attend(x, idx, cnt, stream=s)]
+        if x.shape[2] == 40:
+            out += rope(x, x, pos, stream=s)
+            out += rope.backward(x, x, x, x, pos, stream=s)
+        return out
+
+    want = [both(i, None) for i in range(4)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s in side:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(3_000_000)
+    for _ in range(5):
+        for i in range(4):
+            got.append((i, both(i, side[i % 2])))
+            for w in want[i]:
+                torch.full_like(w, 7)                      # on the current stream, dropped at once
+            torch.full((4 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for i, out in got:
+        for a, b in zip(out, want[i]):
+            assert torch.equal(a, b)
+    svsa.svsa_sync_status()
+
+
+def test_a_chain_on_one_side_stream():
+    """append, select, attend and reset through `stream=` alone, against the current stream's."""
+    B, heads, d = 2, 2, 64
+    plain, chained = (svsa.BlockCache(B, heads, d, 500, code="i8") for _ in range(2))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1_000_000)
+    outs = [[], []]
+    xs = [torch.randn(B, heads, 100, d, generator=_gen(70 + i)).to(BF).cuda() for i in range(4)]
+    s.wait_stream(torch.cuda.current_stream())
+    for c, st, out in ((plain, None, outs[0]), (chained, s, outs[1])):
+        for x in xs:
+            c.append(x, x, stream=st)
+            idx, cnt = c.select(x, 3, stream=st)
+            out += [idx, cnt, c.attend(x, idx, cnt, stream=st), c.attend(x, stream=st)]
+    torch.cuda.synchronize()
+    assert plain.length.tolist() == chained.length.tolist() == [400, 400]
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    chained.reset(stream=s)
+    o = chained.attend(xs[0], stream=s)
+    torch.cuda.synchronize()
+    assert torch.all(o == 0) and chained.length.tolist() == [0, 0]
+    svsa.svsa_sync_status()

@@ -206,7 +206,8 @@ class SparseVideoAttention:
             layer, pos = self.norm_rope
             if not v.is_contiguous():
                 raise ValueError("v must be contiguous [B, heads, N, d] (q and k may be views)")
-            layer(q, k, pos, perm=b.perm, out=(b.qp, b.kp), stream=stream)
+            with torch.no_grad():                  # (the layer has no backward, here as without norm_rope)
+                layer(q, k, pos, perm=b.perm, out=(b.qp, b.kp), stream=stream)
         else:
             svsa_reorder(q, b.qp, b.perm, self.shape, stream)
             svsa_reorder(k, b.kp, b.perm, self.shape, stream)

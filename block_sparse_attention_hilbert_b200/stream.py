@@ -61,8 +61,27 @@ def _on(stream, device):
         yield keep
 
 
+class _NormRopeGrad(torch.autograd.Function):
+    """NormRope.__call__ with its gradients (svsa_qk_norm_rope_bwd)."""
+
+    @staticmethod
+    def forward(ctx, layer, q, k, wq, wk, pos, perm, iperm):
+        ctx.layer, ctx.rows = layer, None if perm is None else perm.shape[0]
+        ctx.save_for_backward(q, k, wq, wk, pos, iperm)
+        return layer._forward(q, k, wq, wk, pos, perm, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        q, k, wq, wk, pos, iperm = ctx.saved_tensors
+        gq, gk = gq.contiguous(), None if k is None else gk.contiguous()
+        dq, dk, dwq, dwk = ctx.layer._backward(gq, gk, q, k, wq, wk, pos, iperm, ctx.rows, None)
+        return None, dq, dk, None if wq is None else dwq, None if wk is None else dwk, None, None, None
+
+
 class NormRope:
-    """Per-head RMS norm and position rotation of queries and keys (svsa_qk_norm_rope), with its weights and tables."""
+    """Per-head RMS norm and position rotation of queries and keys (svsa_qk_norm_rope), with its weights and tables.
+    Differentiable in q, k and the weights."""
 
     def __init__(self, d: int, *, pairs=(), rows: int = 0, theta: float = 10000.0, halves: bool = False, eps: float = 1e-6,
                  wq=None, wk=None, device="cuda"):
@@ -79,21 +98,35 @@ class NormRope:
     def params(self, q, k, pos, rows=None):
         return norm_rope_params(q, k, self.cos, pos, rows=rows, pairs=self.pairs, halves=self.halves, eps=self.eps)
 
-    def __call__(self, q, k, pos=None, *, perm=None, out=None, stream=None):
+    def __call__(self, q, k, pos=None, *, perm=None, iperm=None, out=None, stream=None):
         """q [B, heads_q, N, d], k [B, heads_k, N, d] or None: views with a contiguous last dimension.  perm int32 [rows]:
-        token of each output row (-1: zeros).  Returns (yq, yk) [B, heads, rows, d], into `out` if given."""
+        token of each output row (-1: zeros).  Returns (yq, yk) [B, heads, rows, d], into `out` if given.
+
+        Where q, k or a weight requires gradients the outputs carry them; with a perm that takes its inverse too (iperm
+        int32 [N], the output row of each token, -1 for none; no token may have two), and `out` is not possible.  As with any
+        function of torch, drop the eager graphs of the same leaves before a backward is captured into a CUDA graph."""
         if stream is not None:
             with _on(stream, q.device) as keep:
-                y = self(q, k, pos, perm=perm, out=out)
+                y = self(q, k, pos, perm=perm, iperm=iperm, out=out)
                 if out is None:
                     keep(*y)
                 return y
+        wq, wk = self.wq, self.wk if k is not None else None
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, wq, wk)):
+            if out is not None:
+                raise RuntimeError("an input requires gradients, which outputs given by the caller cannot carry: leave `out` "
+                                   "away, or call under torch.no_grad()")
+            if perm is not None and iperm is None:
+                raise ValueError("an input requires gradients: with a perm, its inverse iperm is needed")
+            return _NormRopeGrad.apply(self, q, k, wq, wk, pos, perm, iperm)
+        return self._forward(q, k, wq, wk, pos, perm, out)
+
+    def _forward(self, q, k, wq, wk, pos, perm, out):
         rows = q.shape[2] if perm is None else perm.shape[0]
         if out is None:
             out = tuple(None if x is None else torch.empty((x.shape[0], x.shape[1], rows, x.shape[3]), dtype=x.dtype, device=x.device)
                         for x in (q, k))
-        svsa_qk_norm_rope(q, k, self.wq, self.wk if k is not None else None, self.cos, self.sin, pos, perm, *out,
-                          self.params(q, k, pos, rows))
+        svsa_qk_norm_rope(q, k, wq, wk, self.cos, self.sin, pos, perm, *out, self.params(q, k, pos, rows))
         return out
 
     def backward(self, gq, gk, q, k, pos=None, *, iperm=None, rows=None, out=None, stream=None):
@@ -105,14 +138,16 @@ class NormRope:
                 dx = self.backward(gq, gk, q, k, pos, iperm=iperm, rows=rows, out=out)
                 keep(*(dx if out is None else dx[2:]))
                 return dx
+        return self._backward(gq, gk, q, k, self.wq, self.wk if k is not None else None, pos, iperm, rows, out)
+
+    def _backward(self, gq, gk, q, k, wq, wk, pos, iperm, rows, out):
         p = self.params(q, k, pos, rows)
         if out is None:
             out = tuple(None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
         dw = torch.empty((2, self.d), dtype=torch.float32, device=q.device)
         ws = torch.empty(svsa_qk_norm_rope_bwd_workspace_bytes(p), dtype=torch.uint8, device=q.device)
         dwk = dw[1] if k is not None else None
-        svsa_qk_norm_rope_bwd(gq, gk, q, k, self.wq, self.wk if k is not None else None, self.cos, self.sin, pos, iperm,
-                              *out, dw[0], dwk, p, ws, ws.numel())
+        svsa_qk_norm_rope_bwd(gq, gk, q, k, wq, wk, self.cos, self.sin, pos, iperm, *out, dw[0], dwk, p, ws, ws.numel())
         return (*out, dw[0], dwk)
 
 

@@ -268,3 +268,60 @@ def test_a_chain_on_one_side_stream():
     torch.cuda.synchronize()
     assert torch.all(o == 0) and chained.length.tolist() == [0, 0]
     svsa.svsa_sync_status()
+
+
+# ---- gradients through autograd ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("order", [False, True])
+@pytest.mark.parametrize("dtype,halves", [(BF, True), (HF, False)])
+def test_autograd_of_norm_and_rotation(dtype, halves, order):
+    """Gradients of a fused projection's output and of the weights, through autograd: those of the call itself, on the
+    current stream and on another."""
+    B, hq, hk, N, d = 2, 6, 2, 70, 64
+    pos = torch.arange(N, dtype=torch.int32, device="cuda").view(1, N, 1)
+    perm = iperm = None
+    if order:
+        perm = torch.cat([torch.randperm(N, generator=_gen(80)), torch.full((58,), -1)]).to(torch.int32).cuda()
+        iperm = torch.argsort(perm[:N]).to(torch.int32)
+    wq, wk = (torch.nn.Parameter(1 + 0.3 * torch.randn(d, generator=_gen(i)).cuda()) for i in (81, 82))
+    rope = svsa.NormRope(d, pairs=(32,), rows=N, halves=halves, wq=wq, wk=wk)
+    x = torch.randn(B, N, hq + hk, d, generator=_gen(83)).to(dtype).cuda().requires_grad_()
+    rows = N if perm is None else 128
+    gq, gk = (torch.randn(B, h, rows, d, generator=_gen(84)).to(dtype).cuda() for h in (hq, hk))
+    with torch.no_grad():
+        q, k = x[:, :, :hq].transpose(1, 2), x[:, :, hq:].transpose(1, 2)
+        want = rope(q, k, pos, perm=perm)
+        dq, dk, dwq, dwk = rope.backward(gq, gk, q, k, pos, iperm=iperm, rows=rows)
+    side = torch.cuda.Stream()
+    for s in (None, side):
+        side.wait_stream(torch.cuda.current_stream())
+        y = x.grad = wq.grad = wk.grad = None              # (no graph of an earlier stream stays)
+        y = rope(x[:, :, :hq].transpose(1, 2), x[:, :, hq:].transpose(1, 2), pos, perm=perm, iperm=iperm, stream=s)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
+        torch.autograd.backward(y, (gq, gk))
+        torch.cuda.synchronize()
+        assert torch.equal(x.grad, torch.cat([dq, dk], 1).transpose(1, 2))
+        assert torch.equal(wq.grad, dwq) and torch.equal(wk.grad, dwk)
+    # only one output used, its gradient broadcast
+    y = x.grad = wq.grad = wk.grad = None
+    y = rope(x[:, :, :hq].transpose(1, 2), x[:, :, hq:].transpose(1, 2), pos, perm=perm, iperm=iperm)
+    y[1].sum().backward()
+    with torch.no_grad():
+        dq, dk, dwq, dwk = rope.backward(torch.zeros_like(gq), torch.ones_like(gk), q, k, pos, iperm=iperm, rows=rows)
+    assert torch.equal(x.grad, torch.cat([dq, dk], 1).transpose(1, 2)) and torch.equal(wk.grad, dwk)
+    assert torch.all(wq.grad == 0) and torch.all(x.grad[:, :, :hq] == 0)
+    svsa.svsa_sync_status()
+
+
+def test_sparse_layer_with_weights_that_require_gradients():
+    """A layer used for inference, its norm weights parameters: it runs, as it does on inputs that require gradients."""
+    B, h, T, H, W, d = 1, 2, 3, 8, 10, 128
+    q, k, v = (torch.randn(B, h, T * H * W, d, generator=_gen(90 + i)).to(BF).cuda() for i in range(3))
+    rope = svsa.NormRope(d, wq=torch.nn.Parameter(torch.linspace(0.8, 1.2, d).cuda()))
+    kw = dict(order="raster", select="topk", keep_frac=0.5)
+    o = svsa.SparseVideoAttention(B, h, T, H, W, d, norm_rope=(rope, None), **kw)(q, k, v)
+    with torch.no_grad():
+        want = svsa.SparseVideoAttention(B, h, T, H, W, d, **kw)(*rope(q, k), v)
+    svsa.svsa_sync_status()
+    assert torch.equal(o, want)

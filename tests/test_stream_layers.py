@@ -77,3 +77,47 @@ def test_a_call_on_a_stream_does_all_its_work_there(streams, name):
         del log[:]
     call(None)
     assert log and all(now is None and given is None for _, now, given in log)
+
+
+def test_norm_and_rotation_record_their_gradients(monkeypatch):
+    """Outputs of inputs or weights that require gradients have a grad_fn, whose backward is the library's; what cannot
+    carry gradients is refused."""
+    B, h, N, d = 1, 2, 5, 64
+    seen = []
+
+    def bwd(gq, gk, q, k, wq, wk, cos, sin, pos, iperm, dq, dk, dwq, dwk, p, ws, n, stream=None):
+        seen.append((gq, gk, p.rows, iperm))
+        dq.fill_(2), dwq.fill_(4)
+        if k is not None:
+            dk.fill_(3), dwk.fill_(5)
+
+    monkeypatch.setattr(layers, "svsa_qk_norm_rope", lambda *a, **kw: None)
+    monkeypatch.setattr(layers, "svsa_qk_norm_rope_bwd", bwd)
+    w = torch.ones(d, requires_grad=True)
+    rope = svsa.NormRope(d, wq=w, device="cpu")
+    x = torch.zeros(B, N, 2 * h, d, dtype=torch.bfloat16)
+    q, k = x[:, :, :h].transpose(1, 2), x[:, :, h:].transpose(1, 2)
+    yq, yk = rope(q, k)                                    # the weight alone requires gradients
+    (yq.float().sum() + 2 * yk.float().sum()).backward()
+    assert torch.all(w.grad == 4) and torch.all(seen[0][0] == 1) and torch.all(seen[0][1] == 2)
+    assert seen[0][0].is_contiguous() and seen[0][1].is_contiguous()
+    x.requires_grad_()
+    perm = torch.tensor([4, 3, 2, 1, 0, -1], dtype=torch.int32)
+    iperm = torch.tensor([4, 3, 2, 1, 0], dtype=torch.int32)
+    q, k = x[:, :, :h].transpose(1, 2), x[:, :, h:].transpose(1, 2)
+    yq, yk = rope(q, k, perm=perm, iperm=iperm)
+    assert yq.shape == yk.shape == (B, h, 6, d)
+    yk.float().sum().backward()                            # (nothing comes back to yq: zeros)
+    assert torch.all(x.grad[:, :, :h] == 2) and torch.all(x.grad[:, :, h:] == 3)
+    assert torch.all(seen[1][0] == 0) and seen[1][2] == 6 and torch.equal(seen[1][3], iperm)
+    y, none = rope(q, None)
+    assert none is None
+    y.float().sum().backward()
+    assert torch.all(x.grad[:, :, :h] == 4)
+    with pytest.raises(ValueError):
+        rope(q, k, perm=perm)
+    out = (torch.empty(B, h, N, d, dtype=torch.bfloat16), torch.empty(B, h, N, d, dtype=torch.bfloat16))
+    with pytest.raises(RuntimeError):
+        rope(q, k, out=out)
+    with torch.no_grad():
+        assert rope(q, k, out=out)[0] is out[0] and not rope(q, k)[0].requires_grad

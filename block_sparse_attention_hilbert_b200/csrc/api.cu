@@ -885,11 +885,16 @@ svsa_status svsa_selftest_timeout(int32_t wait_us, void* stream) {
 
 namespace {
 
-svsa_status check_strides(const int64_t stride[3], const char* name) {
+// Strides of a [B, heads, tokens, d] view.  That of a dimension of size 1 is
+// never a step, so it may be anything; the kernels get 0.
+svsa_status take_strides(const int32_t size[3], const int64_t stride[3], long long out[3], const char* name) {
   for (int e = 0; e < 3; ++e) {
+    out[e] = 0;
+    if (size[e] == 1) continue;
     if (stride[e] < 0 || stride[e] % 8 != 0)
       return fail(SVSA_ERR_INVALID_ARG, "%s[%d]=%lld must be a multiple of 8, >= 0", name, e, (long long)stride[e]);
     if (stride[e] > (1LL << 40)) return fail(SVSA_ERR_UNSUPPORTED, "%s[%d]=%lld", name, e, (long long)stride[e]);
+    out[e] = stride[e];
   }
   return SVSA_OK;
 }
@@ -933,8 +938,9 @@ svsa_status rope_args(const svsa_norm_rope* p, NormRopeArgs* a) {
     a->split1 = p->pairs[0];
     a->split2 = p->axes > 1 ? p->pairs[0] + p->pairs[1] : p->d / 2;
   }
-  SVSA_TRY(check_strides(p->q_stride, "q_stride"));
-  if (p->heads_k > 0) SVSA_TRY(check_strides(p->k_stride, "k_stride"));
+  const int32_t qs[3] = {p->B, p->heads_q, p->N}, ks[3] = {p->B, p->heads_k, p->N};
+  SVSA_TRY(take_strides(qs, p->q_stride, a->stride[0], "q_stride"));
+  if (p->heads_k > 0) SVSA_TRY(take_strides(ks, p->k_stride, a->stride[1], "k_stride"));
   if ((long long)p->B * std::max(p->rows, p->N) >= (1LL << 31) || (long long)p->heads_q + p->heads_k > 32768)
     return fail(SVSA_ERR_UNSUPPORTED, "too many rows or heads for one call");
   a->heads[0] = p->heads_q;
@@ -947,12 +953,6 @@ svsa_status rope_args(const svsa_norm_rope* p, NormRopeArgs* a) {
   a->halves = p->pairing;
   a->eps = p->eps;
   a->pos_stride = p->pos_stride;
-  for (int e = 0; e < 3; ++e) {
-    a->stride[0][e] = p->q_stride[e];
-    a->stride[1][e] = p->k_stride[e];
-    a->out_stride[0][e] = p->dq_stride[e];
-    a->out_stride[1][e] = p->dk_stride[e];
-  }
   return SVSA_OK;
 }
 
@@ -1057,14 +1057,14 @@ svsa_status svsa_qk_norm_rope_bwd(const void* dyq, const void* dyk, const void* 
   SVSA_TRY(rope_args(p, &a));
   SVSA_TRY(rope_inputs(p, &a, q, k, wq, wk, cos, sin, pos, imap, "imap"));
   const int32_t qs[3] = {p->B, p->heads_q, p->N}, ks[3] = {p->B, p->heads_k, p->N};
-  SVSA_TRY(check_strides(p->dq_stride, "dq_stride"));
+  SVSA_TRY(take_strides(qs, p->dq_stride, a.out_stride[0], "dq_stride"));
   SVSA_TRY(check_apart(qs, p->dq_stride, p->d, "dq_stride"));
   SVSA_PTR(dyq, "dyq");
   SVSA_PTR(dq, "dq");
   a.dy[0] = dyq;
   a.out[0] = dq;
   if (p->heads_k > 0) {
-    SVSA_TRY(check_strides(p->dk_stride, "dk_stride"));
+    SVSA_TRY(take_strides(ks, p->dk_stride, a.out_stride[1], "dk_stride"));
     SVSA_TRY(check_apart(ks, p->dk_stride, p->d, "dk_stride"));
     SVSA_PTR(dyk, "dyk");
     SVSA_PTR(dk, "dk");
@@ -1094,8 +1094,10 @@ svsa_status svsa_cache_append(const svsa_cache* c, const void* k, const void* v,
   if (p == nullptr) return fail(SVSA_ERR_INVALID_ARG, "params is NULL");
   if (p->N < 1) return fail(SVSA_ERR_INVALID_ARG, "N=%d must be >= 1", p->N);
   if (p->dtype != SVSA_BF16 && p->dtype != SVSA_F16) return fail(SVSA_ERR_UNSUPPORTED, "dtype=%d unknown", p->dtype);
-  SVSA_TRY(check_strides(p->k_stride, "k_stride"));
-  SVSA_TRY(check_strides(p->v_stride, "v_stride"));
+  const int32_t size[3] = {c->B, c->heads, p->N};
+  long long ks[3], vs[3];
+  SVSA_TRY(take_strides(size, p->k_stride, ks, "k_stride"));
+  SVSA_TRY(take_strides(size, p->v_stride, vs, "v_stride"));
   if (((long long)p->N / kBlock + 2) * c->heads * c->B >= (1LL << 30))
     return fail(SVSA_ERR_UNSUPPORTED, "too many blocks for one call");
   SVSA_PTR(k, "k");
@@ -1106,11 +1108,6 @@ svsa_status svsa_cache_append(const svsa_cache* c, const void* k, const void* v,
     return fail(SVSA_ERR_INVALID_ARG, "len_out must not alias len or n_new");
   if (c->k == c->v || c->k_scale == c->v_scale)
     return fail(SVSA_ERR_INVALID_ARG, "keys and values must have codes and scales of their own");
-  long long ks[3], vs[3];
-  for (int e = 0; e < 3; ++e) {
-    ks[e] = p->k_stride[e];
-    vs[e] = p->v_stride[e];
-  }
   return cuda_status(counted(launch_cache_append(a, k, v, ks, vs, n_new, len_out, p->N, p->dtype == SVSA_F16,
                                                  (cudaStream_t)stream), 1),
                      "cache_append launch");

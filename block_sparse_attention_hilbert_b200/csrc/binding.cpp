@@ -63,12 +63,14 @@ void* dense(const at::Tensor* t, at::ScalarType type, std::initializer_list<int6
   return t->data_ptr();
 }
 
-// The address of a view [B, heads, N, d] with these strides and a contiguous last dimension.
+// The address of a view [B, heads, N, d] with these strides (where a dimension is not of size 1) and a contiguous last
+// dimension.
 void* view(const at::Tensor* t, at::ScalarType type, std::initializer_list<int64_t> shape, const int64_t stride[3],
            int device, const char* name) {
   if (t == nullptr) return nullptr;
-  if (t->scalar_type() != type || !same(t->sizes(), shape) || t->get_device() != device ||
-      !same(t->strides(), {stride[0], stride[1], stride[2], 1}))
+  bool fits = t->scalar_type() == type && same(t->sizes(), shape) && t->get_device() == device && t->stride(3) == 1;
+  for (int e = 0; fits && e < 3; ++e) fits = t->size(e) == 1 || t->stride(e) == stride[e];
+  if (!fits)
     fail(std::string(name) + ": expected " + c10::toString(type) + " " + text(at::IntArrayRef(shape.begin(), shape.size())) +
          " as in the parameters, with a contiguous last dimension, on device " + std::to_string(device) + ", got " + got(*t));
   return t->data_ptr();

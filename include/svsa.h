@@ -498,7 +498,8 @@ typedef struct {
   float eps;                    /* >= 0 */
   int64_t pos_stride;           /* int32 elements between the batches' positions; 0 = shared */
   int64_t q_stride[3];          /* elements between batches, heads and tokens of q ... */
-  int64_t k_stride[3];          /* ... and of k: multiples of 8; a row's d values are contiguous */
+  int64_t k_stride[3];          /* ... and of k: multiples of 8 (anything for a dimension of
+                                   size 1); a row's d values are contiguous */
   int64_t dq_stride[3];         /* svsa_qk_norm_rope_bwd: the same of dq and dk */
   int64_t dk_stride[3];
 } svsa_norm_rope;
@@ -560,7 +561,7 @@ typedef struct {
 typedef struct {
   int32_t N;                  /* tokens per sequence in k and v */
   int32_t dtype;              /* svsa_dtype */
-  int64_t k_stride[3];        /* elements between batches, heads and tokens: multiples of 8 */
+  int64_t k_stride[3];        /* elements between batches, heads and tokens: as in svsa_norm_rope */
   int64_t v_stride[3];
 } svsa_cache_tokens;
 

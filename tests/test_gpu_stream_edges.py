@@ -325,3 +325,27 @@ def test_sparse_layer_with_weights_that_require_gradients():
         want = svsa.SparseVideoAttention(B, h, T, H, W, d, **kw)(*rope(q, k), v)
     svsa.svsa_sync_status()
     assert torch.equal(o, want)
+
+
+# ---- strides of dimensions of size 1 ------------------------------------------------------------
+
+def test_strides_of_dimensions_of_size_one_do_not_matter():
+    """A batch, head or token dimension of size 1 may have any stride: nothing is ever a step away along it."""
+    d = 64
+    x = torch.randn(3, 1, 5, d, generator=_gen(46)).to(BF).cuda()
+    q = x[1:2].as_strided((1, 1, 5, d), (3, 5, d, 1), x.stride(0))
+    t = x[0, 0, :1].as_strided((1, 1, 1, d), (1, 2, 3, 1))
+    for a in (q, t):
+        rope = svsa.NormRope(d)
+        want = rope(a.contiguous().clone(), a.contiguous().clone())
+        got = rope(a, a)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        g = torch.randn(a.shape, generator=_gen(47)).to(BF).cuda()
+        for u, w in zip(rope.backward(g, g, a, a), rope.backward(g, g, a.contiguous().clone(), a.contiguous().clone())):
+            assert torch.equal(u, w)
+        caches = [svsa.BlockCache(1, 1, d, 64) for _ in range(2)]
+        caches[0].append(a, a)
+        caches[1].append(a.contiguous().clone(), a.contiguous().clone())
+        for u, w in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v)):
+            assert torch.equal(u.view(torch.uint8), w.view(torch.uint8))
+    svsa.svsa_sync_status()

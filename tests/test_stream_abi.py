@@ -251,3 +251,24 @@ def test_rope_tables_and_grid_positions():
     pos = svsa.grid_positions(2, 3, 4, frame=5, device="cpu")
     assert pos.shape == (1, 24, 3) and pos[0, 0].tolist() == [5, 0, 0] and pos[0, 23].tolist() == [6, 2, 3]
     assert pos[0, 1 * 12 + 2 * 4 + 1].tolist() == [6, 2, 1]
+
+
+def test_strides_of_dimensions_of_size_one_are_not_looked_at():
+    """A dimension of size 1 is never stepped along (each call gets as far as the missing pointer)."""
+    odd = (3, 640, 64)
+    for p in (_rope(q_stride=odd), _rope(k_stride=(-7, 640, 64)), _rope(heads_q=1, q_stride=(1, 1 << 50, 64)),
+              _rope(N=1, rows=1, q_stride=(2560, 64, 1), k_stride=(0, 64, 3))):
+        assert _fwd(p, yq=None) == 1 and "yq is NULL" in _err()
+    for p in (_rope(dq_stride=odd), _rope(dk_stride=(-1, 640, 64))):
+        assert _bwd(p, ws=None) == 1 and "ws is NULL" in _err()
+    c = _cache(B=1, heads=1)
+    assert _append(c, N=1, ks=(1, 2, 3), vs=(-1, 5, 7), k=None) == 1 and "k is NULL" in _err()
+    # those of the others still are
+    assert _fwd(_rope(q_stride=(3, 641, 64))) == 1 and _append(c, N=2, ks=(1, 2, 3)) == 1
+    # and a view may differ from the parameters' tensor there
+    q = torch.zeros(1, 4, 3, 64, dtype=torch.bfloat16)
+    other = torch.zeros(7, 4, 3, 64, dtype=torch.bfloat16)[::7].as_strided((1, 4, 3, 64), (5, 192, 64, 1))
+    p = svsa.norm_rope_params(q, None)
+    for x in (q, other):                                   # (as far as the device)
+        with pytest.raises(ValueError, match="CUDA"):
+            svsa.svsa_qk_norm_rope(x, None, None, None, None, None, None, None, torch.empty_like(q), None, p)

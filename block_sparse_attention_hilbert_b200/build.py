@@ -101,7 +101,6 @@ def build(jobs: int = 0, force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(jobs + 1) as ex:
         binding = ex.submit(_compile_binding, force)
         results = list(ex.map(lambda s: _compile(nvcc, s, force, verbose), srcs))
-        binding_obj = binding.result()
     logs = [log for _, log in results if log.strip()]
     objs = [o for o, _ in results]
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
@@ -109,10 +108,11 @@ def build(jobs: int = 0, force: bool = False, verbose: bool = False) -> str:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    _link_binding(binding_obj, force)
     if verbose:
         for log in logs:
             sys.stderr.write(log)
+    # last: without Python's or torch's headers the C library is there all the same, and the failure is reported
+    _link_binding(binding.result(), force)
     return LIB
 
 

@@ -121,3 +121,33 @@ def test_norm_and_rotation_record_their_gradients(monkeypatch):
         rope(q, k, out=out)
     with torch.no_grad():
         assert rope(q, k, out=out)[0] is out[0] and not rope(q, k)[0].requires_grad
+
+
+def test_the_library_is_built_without_the_python_module(tmp_path, monkeypatch):
+    """Where the Python module does not compile (no Python.h), the C library is linked first and the failure is raised."""
+    import ctypes
+    import shutil
+    import subprocess
+
+    from block_sparse_attention_hilbert_b200 import build
+    try:
+        build._nvcc()
+    except RuntimeError:
+        pytest.skip("nvcc not available")
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
+    src, obj = tmp_path / "one.c", tmp_path / "one.o"
+    src.write_text("int svsa_one(void) { return 1; }\n")
+    subprocess.run(["gcc", "-fPIC", "-c", str(src), "-o", str(obj)], check=True)
+
+    def no_headers(force):
+        raise RuntimeError("Python.h: no such file")
+
+    for name, value in (("BUILD", str(tmp_path)), ("LIBDIR", str(tmp_path)), ("LIB", str(tmp_path / "libsvsa.so")),
+                        ("BINDING", str(tmp_path / "_svsa_binding.so")), ("_compile", lambda *a: (str(obj), "")),
+                        ("_compile_binding", no_headers)):
+        monkeypatch.setattr(build, name, value)
+    monkeypatch.setattr(build.glob, "glob", lambda pattern: ["one.cu"])
+    with pytest.raises(RuntimeError, match="Python.h"):
+        build.build()
+    assert ctypes.CDLL(str(tmp_path / "libsvsa.so")).svsa_one() == 1

@@ -364,6 +364,16 @@ struct Cta {
   static_assert(kRows * kPitch * 4 <= kRing * kTile, "the sums fit the ring");
 };
 
+// After a wait that gave up: the warp's copies in flight (tiles used ..
+// issued - 1), each waited for with a limit of its own, before the ring holds
+// anything else or the CTA goes.
+__device__ __noinline__ void wait_in_flight(uint32_t bar, uint32_t ring, uint32_t used, uint32_t issued) {
+  for (uint32_t x = used; x < issued; ++x) {
+    volatile uint32_t no_abort = 0u;
+    tc::wait_bar(bar + 8 * (x % ring), (x / ring) & 1u, &no_abort, 96);
+  }
+}
+
 // A finished row's four columns from col on, or the CTA's share of them.
 template <int D, typename T>
 __device__ __forceinline__ void write_out(const AttnArgs& p, const Segment& s, int t, int hg, int col, float4 x, float top,
@@ -474,8 +484,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     };
     auto arrived = [&]() -> uint32_t {        // the next tile in order
       const uint32_t slot = used % RING, parity = (used / RING) & 1u;
-      if (alive) alive = tc::wait_bar(bar + 8 * slot, parity, dead, 95);
-      alive = __all_sync(0xffffffffu, alive);
+      if (alive) {
+        alive = __all_sync(0xffffffffu, tc::wait_bar(bar + 8 * slot, parity, dead, 95));
+        if (!alive) wait_in_flight(bar, RING, used, issued);
+      }
       ++used;
       return ring + slot * TILE;
     };

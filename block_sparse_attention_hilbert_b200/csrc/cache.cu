@@ -16,10 +16,10 @@
 //   in 8 bits with power-of-two scales: an integer dot product below 2^21
 //   times a power of two, exact in fp32, so that no list depends on the order
 //   of a sum and equal scores are really equal (the lower index wins).  Each
-//   CTA scores a range of blocks, one thread per block (its mean is one
-//   128-byte line), and puts the sortable keys into the first CTA's shared
-//   memory; that one finds the cap-th largest key by three digits of 11, 11
-//   and 10 bits and writes the list in ascending order.
+//   CTA scores a range of blocks, a warp 32 of them at a time (d / 16 lanes
+//   read a mean of d bytes together), and puts the sortable keys into the
+//   first CTA's shared memory; that one finds the cap-th largest key by three
+//   digits of 11, 11 and 10 bits and writes the list in ascending order.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
@@ -67,16 +67,10 @@ __device__ __forceinline__ void unpack8<__half>(uint4 v, float x[8]) {
   }
 }
 
-// The code of y = x / scale, rounded to nearest even and saturated; NaN gives 0.
-template <bool I8>
-__device__ __forceinline__ uint32_t encode(float y) {
+// The int8 code of y, rounded to nearest even and saturated; NaN gives 0.
+__device__ __forceinline__ uint32_t encode_i8(float y) {
   if (y != y) return 0u;
-  if constexpr (I8) {
-    const int c = __float2int_rn(fminf(fmaxf(y, -127.f), 127.f));
-    return (uint32_t)c & 0xffu;
-  } else {
-    return (uint32_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-  }
+  return (uint32_t)__float2int_rn(fminf(fmaxf(y, -127.f), 127.f)) & 0xffu;
 }
 
 // max |x| of packed pairs, NaN and infinities kept.
@@ -301,7 +295,7 @@ __global__ void __launch_bounds__(kAppendThreads, 7) cache_append_kernel(const _
 #pragma unroll
     for (int i = 1; i < D / 32; ++i) top = fmaxf(top, wtop[i]);
     const float s = pow2_scale(top, true);
-    p.c.mean[cell * D + threadIdx.x] = (int8_t)encode<true>(s > 0.f ? mean / s : 0.f);
+    p.c.mean[cell * D + threadIdx.x] = (int8_t)encode_i8(s > 0.f ? mean / s : 0.f);
     if (threadIdx.x == 0) p.c.mean_scale[cell] = s * kUnit * scale;
   }
 }
@@ -387,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 5) cache_select_kernel(const __grid_
     const float s = pow2_scale(warp_max(amax), true), inv = s > 0.f ? 1.f / s : 0.f;
     uint32_t w = 0u;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) w |= encode<true>(v[e] * inv) << (8 * e);
+    for (int e = 0; e < D / 32; ++e) w |= encode_i8(v[e] * inv) << (8 * e);
     if constexpr (D == 128) qc[g * (D / 4) + lane] = w;
     else reinterpret_cast<uint16_t*>(qc + g * (D / 4))[lane] = (uint16_t)w;
     if (lane == 0) qs[g] = s;

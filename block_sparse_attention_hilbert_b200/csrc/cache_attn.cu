@@ -13,8 +13,10 @@
 // fp16 is exact, fp16 x fp16 products are exact in fp32), and up to eight
 // query rows cost half of what a tile of 16 query rows would.
 //
-// More than 32 (d = 64: 48) query rows per key head take the 128-row tcgen05
-// tiles of cache_attn_rows.cuh instead, over the same items and shares.
+// More than 32 (d = 64: 48) query rows per key head, and in large caches more
+// than 16 (see tile_rows), take the 128-row tcgen05 tiles of
+// cache_attn_rows.cuh instead, over the same items and shares.  So do lists of
+// many queries, gathered per tile (see gather_plan).
 //
 // Work: an item is (sequence, key head, tile of 8 or 16 rows), or with lists
 // (sequence, query, key head, tile of the group's rows); a unit is one
@@ -22,11 +24,11 @@
 // shares of all units, so ragged lengths balance; an item that several CTAs
 // share is joined by a second kernel from fp32 partial sums with their maxima,
 // in CTA order.  Where items are short, or so many that whole ones balance,
-// each goes to one CTA and there is no second kernel.  In a CTA, twelve warps (eight with 16 rows)
-// take the blocks of a segment in turn, each with a ring of its own of tiles
-// filled by TMA (128-byte swizzle, so that both the row-wise reads of K and
-// the column-wise reads of V are free of bank conflicts), and no barrier until
-// the segment's end.
+// each goes to one CTA and there is no second kernel.  In a CTA, twelve warps
+// (eight with 16 rows) take the blocks of a segment in turn, each with a ring
+// of its own of tiles filled by TMA (swizzled over the row, so that both the
+// row-wise reads of K and the column-wise reads of V are free of bank
+// conflicts), and no barrier until the segment's end.
 //
 // Rounding: q is scaled per row by a power of two into fp16 (exact for bf16
 // values within 2^-14 of the row's largest; below that they keep 2^-24 of it);
@@ -963,10 +965,6 @@ int tile_rows(long long rows, bool lists, const CacheArgs& c) {
   const double more = ceil_div(rows, 16) * (c.d == 128 ? 0.43 : 0.23) - (c.d == 128 ? 0.72 : 0.62);
   return more * c.B * c.heads * c.max_blocks > 10.0 * kNumSMs ? kTileRows : 16;
 }
-
-}  // namespace
-
-namespace {
 
 // Lists gathered per 128-row tile of queries: the tile visits every block that
 // one of its queries lists, rows masked by a bit per query and block.

@@ -38,24 +38,10 @@ constexpr int kFwdPerSM = 4, kBwdPerSM = 2;     // CTAs per SM that the register
 constexpr int kStages = 3;                 // steps in the backward's ring
 constexpr int kBwdSmem = kStages * 2 * kRowsInFlight * kThreads * 16;
 
-struct NormRope {
-  const void* x[2];                 // q, k
-  const void* dy[2];                // backward: gradients [B, heads, rows, d]
-  void* out[2];                     // forward: [B, heads, rows, d]; backward: dx, strided
-  const float* w[2];                // nullable
-  const float* cos;                 // nullable: no rotation
-  const float* sin;
-  const int32_t* pos;
-  const int32_t* map;               // forward: output row -> token; backward: token -> output row
-  float* part;                      // backward: partial dw rows [CTA][d]
-  long long stride[2][3];           // x: batch, head, token
-  long long out_stride[2][3];       // dx
-  long long pos_stride;
-  int heads[2], chunks[2];          // chunks: head groups of `hb` heads
+// The call's arguments, and how its heads are split.
+struct NormRope : NormRopeArgs {
+  int chunks[2];                    // head groups of `hb` heads
   int hb;
-  int B, N, rows, axes, split1, split2, table_rows;
-  int halves;
-  float eps;
 };
 
 template <typename T>
@@ -170,7 +156,7 @@ template <int D, typename T, bool HALVES, bool TURN>
 __global__ void __launch_bounds__(kThreads, kFwdPerSM) norm_rope_kernel(const __grid_constant__ NormRope p) {
   constexpr int L = D / 8;                      // lanes per row
   const int ch = threadIdx.x % L;
-  const unsigned mask = (L == 32 ? ~0u : ((1u << L) - 1)) << ((threadIdx.x % 32) / L * L);
+  const unsigned mask = ((1u << L) - 1) << ((threadIdx.x % 32) / L * L);
   const unsigned tok = blockIdx.x * (kThreads / L) + threadIdx.x / L;
   if (tok >= (unsigned)(p.B * p.rows)) return;                // uniform over the lane group
   const int which = (int)blockIdx.y >= p.chunks[0];
@@ -264,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSM) norm_rope_bwd_kernel(cons
   __shared__ float red[G][D];
   cudaTriggerProgrammaticLaunchCompletion();    // (the summing kernel may take its place; it waits for this one's end)
   const int ch = threadIdx.x % L, grp = threadIdx.x / L;
-  const unsigned mask = (L == 32 ? ~0u : ((1u << L) - 1)) << ((threadIdx.x % 32) / L * L);
+  const unsigned mask = ((1u << L) - 1) << ((threadIdx.x % 32) / L * L);
   const int which = (int)blockIdx.x >= ctas_q;
   const int cta = which ? (int)blockIdx.x - ctas_q : (int)blockIdx.x;
   const int ctas = (which ? (int)gridDim.x - ctas_q : ctas_q) / p.chunks[which];      // of one head group
@@ -428,38 +414,6 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restr
   }
 }
 
-NormRope fill(const NormRopeArgs& a) {
-  NormRope p{};
-  for (int w = 0; w < 2; ++w) {
-    p.x[w] = a.x[w];
-    p.dy[w] = a.dy[w];
-    p.out[w] = a.out[w];
-    p.w[w] = a.w[w];
-    p.heads[w] = a.heads[w];
-    for (int e = 0; e < 3; ++e) {
-      p.stride[w][e] = a.stride[w][e];
-      p.out_stride[w][e] = a.out_stride[w][e];
-    }
-  }
-  p.cos = a.cos;
-  p.sin = a.sin;
-  p.pos = a.pos;
-  p.map = a.map;
-  p.part = a.part;
-  p.pos_stride = a.pos_stride;
-  p.B = a.B;
-  p.N = a.N;
-  p.rows = a.rows;
-  p.axes = a.axes;
-  p.split1 = a.split1;
-  p.split2 = a.split2;
-  p.table_rows = a.table_rows;
-  p.halves = a.halves;
-  p.eps = a.eps;
-  return p;
-}
-
-
 // Heads per lane group: a token's tables and indices are then read once for
 // that many rows.  One where the call is small and its time is one row's
 // latency, else up to 16, in equal groups of whole loads.
@@ -471,6 +425,12 @@ int pick_hb(const NormRopeArgs& a, long long tokens, int d) {
   if (hb < kRowsInFlight) return hb;
   const int parts = (most + hb - 1) / hb, each = (most + parts - 1) / parts;
   return std::min(hb, (each + kRowsInFlight - 1) / kRowsInFlight * kRowsInFlight);
+}
+
+NormRope plan(const NormRopeArgs& a, long long tokens, int d) {
+  NormRope p{a, {0, 0}, pick_hb(a, tokens, d)};
+  for (int w = 0; w < 2; ++w) p.chunks[w] = (a.heads[w] + p.hb - 1) / p.hb;
+  return p;
 }
 
 template <typename F>
@@ -507,10 +467,8 @@ void bwd_ctas(const NormRopeArgs& a, int d, int hb, int* cq, int* ck) {
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int d, int f16, cudaStream_t st) {
-  NormRope p = fill(a);
   const long long tokens = (long long)a.B * a.rows;
-  p.hb = pick_hb(a, tokens, d);
-  for (int w = 0; w < 2; ++w) p.chunks[w] = (a.heads[w] + p.hb - 1) / p.hb;
+  const NormRope p = plan(a, tokens, d);
   const int G = kThreads / (d / 8);
   const dim3 grid((unsigned)((tokens + G - 1) / G), (unsigned)(p.chunks[0] + p.chunks[1]));
   by_type(d, f16, a.halves, a.cos != nullptr, [&](auto D_, auto z, auto H_, auto R_) {
@@ -526,9 +484,7 @@ size_t norm_rope_bwd_workspace_bytes(const NormRopeArgs& a, int d) {
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, int d, int f16, float* dwq, float* dwk, cudaStream_t st) {
-  NormRope p = fill(a);
-  p.hb = pick_hb(a, (long long)a.B * a.N, d);
-  for (int w = 0; w < 2; ++w) p.chunks[w] = (a.heads[w] + p.hb - 1) / p.hb;
+  const NormRope p = plan(a, (long long)a.B * a.N, d);
   int cq = 0, ck = 0;
   bwd_ctas(a, d, p.hb, &cq, &ck);
   cudaError_t e = cudaSuccess;

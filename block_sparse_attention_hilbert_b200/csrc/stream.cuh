@@ -32,17 +32,17 @@ inline cudaError_t allow_smem(int bytes) {
 constexpr unsigned int kFlagIndex = 8u, kFlagNotFinite = 16u;
 
 struct NormRopeArgs {
-  const void* x[2];
-  const void* dy[2];
-  void* out[2];
-  const float* w[2];
-  const float* cos;
+  const void* x[2];                // q, k
+  const void* dy[2];               // backward: gradients [B, heads, rows, d]
+  void* out[2];                    // forward: [B, heads, rows, d]; backward: dx, strided
+  const float* w[2];               // nullable
+  const float* cos;                // nullable: no rotation
   const float* sin;
   const int32_t* pos;
-  const int32_t* map;
-  float* part;
-  long long stride[2][3];          // inputs
-  long long out_stride[2][3];      // backward: gradients of the inputs
+  const int32_t* map;              // nullable; forward: output row -> token, backward: token -> output row
+  float* part;                     // backward: partial dw rows [CTA][d]
+  long long stride[2][3];          // x: batch, head, token
+  long long out_stride[2][3];      // dx
   long long pos_stride;
   int heads[2];
   int B, N, rows, axes, split1, split2, table_rows, halves;

@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
       const int lim = live && p.causal ? max(len - p.Tq + 1 + t, 0) : len;
 
       float ry = kNone, rs = kNone, l = 0.f;     // references of y and s (log2), row sum against rs
+      float ytop = kNone;                        // the largest y
       // this half's pages, looked up 32 steps at a time, one to a lane, and the
       // next 32 half way through them: block (-1: not there) and scales
       auto look = [&](int i, int* blk, float* ks, float* vs) {
@@ -502,19 +503,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) cache_attn_rows_kernel(const 
         const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
         const bool skip = LISTS && !listed;      // (the row's query does not list this page)
         const float smax = skip ? -INFINITY : edge ? top : top * f;
-        float alpha = 1.f;
         if (smax > -INFINITY) {
-          const float ymax = smax + lv;          // (-inf without values)
-          if (ymax > ry + kRoom) {
-            if (ry != kNone) alpha = ex2(ry - ymax + kHead);      // (else the accumulator holds zeros)
-            ry = ymax - kHead;
-          }
+          ytop = fmaxf(ytop, smax + lv);         // (no larger without values)
+          if (ry == kNone) ry = ytop - kHead;    // (the accumulator holds zeros)
           if (smax > rs + kLazy) {
             l *= ex2(rs - smax);                 // (of the first key: 0 times 0)
             rs = smax;
           }
         }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        if (__any_sync(0xffffffffu, ytop > ry + kRoom)) {
+          // one row's reference has to rise: all of the warp's do, which makes
+          // the next time come later
+          const float to = fmaxf(ry, ytop - kHead), alpha = ex2(ry - to);
+          ry = to;
           // rescale this half's accumulator (factor 1 where nothing changed)
           // once its previous P V product is done; there is one, in this item
           const uint32_t xp = x - 1u, sp = xp % kSBufs;

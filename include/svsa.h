@@ -599,7 +599,8 @@ typedef struct {
  *   score = max over the head's group of  q8 . mean8 * (q's scale * mean_scale),
  * q8 = q in whole numbers under its row's smallest power of two that holds it
  * in 127; up to cap in all, equal scores by the lower index.  Dot products of
- * whole numbers are exact, so the lists depend on nothing but the inputs.
+ * whole numbers are exact, and so are the scores within the range of fp32, so
+ * the lists depend on nothing but the inputs.
  * idx [B, Tq, heads, cap]: ascending, then zeros; cnt [B, Tq, heads].
  * first + last <= cap; max_blocks <= 32768; heads_q / heads <= 128; mean and
  * mean_scale required.  A value of q that is not finite saturates (NaN counts

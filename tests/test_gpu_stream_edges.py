@@ -349,3 +349,36 @@ def test_strides_of_dimensions_of_size_one_do_not_matter():
         for u, w in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v)):
             assert torch.equal(u.view(torch.uint8), w.view(torch.uint8))
     svsa.svsa_sync_status()
+
+
+# ---- the largest selection ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d,group,cap", [(128, 128, 4097), (64, 1, 32767)])
+def test_selection_over_the_most_blocks(d, group, cap):
+    """32,768 blocks and 128 query heads per key head: scores are whole numbers under powers of two, exact in 64 bits."""
+    nb = 32768
+    rng = np.random.default_rng(7)
+    mean = rng.integers(-127, 128, (nb, 1, d)).astype(np.int8)
+    scale = np.exp2(rng.integers(-9, 3, (nb, 1))).astype(np.float32)
+    codes = torch.zeros(nb, 1, 64, d, dtype=torch.int8, device="cuda")
+    one = torch.ones(nb, 1, device="cuda")
+    order = rng.permutation(nb).astype(np.int32)
+    dev = lambda a: torch.from_numpy(a).cuda()
+    n = torch.tensor([64 * nb - 3], dtype=torch.int32, device="cuda")
+    mean_t, scale_t, table = dev(mean), dev(scale), dev(order[None])
+    c = svsa.block_cache(codes, codes.clone(), one, one.clone(), table, n, mean_t, scale_t)
+    q = torch.randn(1, group, 2, d, generator=_gen(50)).to(BF).cuda()
+    idx = torch.full((1, 2, 1, cap), -5, dtype=torch.int32, device="cuda")
+    cnt = torch.full((1, 2, 1), -5, dtype=torch.int32, device="cuda")
+    svsa.svsa_cache_select(c, q, idx, cnt, svsa.cache_query(q, causal=True, cap=cap, first=2, last=3))
+    svsa.svsa_sync_status()
+    for t in range(2):
+        score = np.full(nb, -np.inf)
+        for e in range(group):
+            row = _np(q[0, e, t])
+            s = stream.pow2_scale(np.abs(row).max(), "i8")
+            qi = stream.encode(row, s, "i8").view(np.int8).astype(np.float64)
+            score = np.maximum(score, (mean[order, 0].astype(np.float64) @ qi) * (s * scale[order, 0].astype(np.float64)))
+        score[:2] = score[-3:] = np.inf
+        want = np.sort(np.lexsort((np.arange(nb), -score))[:cap])
+        assert cnt[0, t, 0] == cap and np.array_equal(idx[0, t, 0].cpu().numpy(), want)

@@ -14,10 +14,10 @@
 // step, with a maximum, a row sum and an accumulator of their own, merged at
 // the item's end; warps 2, 3 and 12-15 widen the pages.  Measured on 1560
 // queries x 12 heads over 32,760 tokens: 694 us with one page to a step, 645
-// with two, 554 with the next step's K widened before this one's V, 408 (771
-// TFLOP/s) with the copies and the tables in a warp of their own, which looks
-// 32 blocks up at a time (510 with both in a seventh widening warp, whose
-// time every stage then waits for).
+// with two, 554 with the next step's K widened before this one's V, 404 to 416
+// (755 to 778 TFLOP/s) with the copies and the tables in a warp of their own,
+// which looks 32 blocks up at a time (510 with both in a seventh widening warp,
+// whose time every stage then waits for).
 //
 // Scales: the key scale joins the softmax's factor.  The value scale goes
 // into the weights as an exponent, P = 2^(y - m'), y = s + log2 vs, with a
@@ -28,8 +28,11 @@
 // not touch m', and its terms of the row sum are taken on their own.  Both
 // references are lazy.  That of s is raised when passed by 2^12.  m' is put
 // 2^11 below the largest y and raised when a y passes it by 2^15 (fp16 ends at
-// 2^16), so that weights down to 2^-36 of the largest keep a value and those
-// down to 2^-25 all of fp16's bits: a tail below one dominant key counts.
+// 2^16), so that weights down to 2^-35 of the largest keep a value and those
+// down to 2^-25 all of fp16's bits: a tail below one dominant key counts.  When
+// one row's m' has to rise, all of its warp's do: with each at its own time, 60
+// queries x 12 heads over 32,760 tokens took 54.3 us, now 53.0 (51.7 with m' at
+// the largest y and 2^12 of room, which lost such tails).
 //
 // Bound by the hand-offs of a step (S, softmax, P V): without the widening the
 // same loop takes nine tenths of the time.

@@ -50,6 +50,8 @@ def _on(stream, device):
     was current, where the caller will use them."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    if stream.device != device:                            # (the tensors' allocations and launches would not be on it)
+        raise ValueError(f"the stream is one of {stream.device}, the tensors are on {device}")
     caller = torch.cuda.current_stream(device)
 
     def keep(*tensors):
@@ -112,7 +114,8 @@ class NormRope:
                     keep(*y)
                 return y
         wq, wk = self.wq, self.wk if k is not None else None
-        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, wq, wk)):
+        if torch.is_grad_enabled() and (q.requires_grad or k is not None and k.requires_grad or
+                                        wq is not None and wq.requires_grad or wk is not None and wk.requires_grad):
             if out is not None:
                 raise RuntimeError("an input requires gradients, which outputs given by the caller cannot carry: leave `out` "
                                    "away, or call under torch.no_grad()")
@@ -152,7 +155,8 @@ class NormRope:
 
 
 class BlockCache:
-    """Keys and values of B sequences in 8-bit pages of 64 tokens (struct svsa_cache), with its buffers."""
+    """Keys and values of B sequences in 8-bit pages of 64 tokens (struct svsa_cache), with its buffers.  For answering, not
+    for training: what it returns carries no gradients."""
 
     def __init__(self, B: int, heads: int, d: int, max_tokens: int, *, code: str = "e4m3", n_pages: int | None = None,
                  table=None, means: bool = True, device="cuda"):

@@ -382,3 +382,36 @@ def test_selection_over_the_most_blocks(d, group, cap):
         score[:2] = score[-3:] = np.inf
         want = np.sort(np.lexsort((np.arange(nb), -score))[:cap])
         assert cnt[0, t, 0] == cap and np.array_equal(idx[0, t, 0].cpu().numpy(), want)
+
+
+def test_autograd_of_norm_and_rotation_captured():
+    """Forward and backward in one CUDA graph, replayed on other values: the eager gradients."""
+    B, hq, hk, N, d = 1, 4, 2, 50, 128
+    pos = torch.arange(N, dtype=torch.int32, device="cuda").view(1, N, 1)
+    wq, wk = (torch.nn.Parameter(1 + 0.3 * torch.randn(d, generator=_gen(i)).cuda()) for i in (91, 92))
+    rope = svsa.NormRope(d, pairs=(64,), rows=N, wq=wq, wk=wk)
+    x = torch.randn(B, N, hq + hk, d, generator=_gen(93)).to(BF).cuda().requires_grad_()
+    gq, gk = (torch.randn(B, h, N, d, generator=_gen(94)).to(BF).cuda() for h in (hq, hk))
+
+    def step():
+        y = rope(x[:, :, :hq].transpose(1, 2), x[:, :, hq:].transpose(1, 2), pos)
+        return torch.autograd.grad(y, (x, wq, wk), (gq, gk))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (95, 96):
+        with torch.no_grad():
+            x.copy_(torch.randn(x.shape, generator=_gen(seed)).to(BF))
+            wq.mul_(1.1)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [g.clone() for g in got]
+        for a, b in zip(kept, step()):
+            assert torch.equal(a, b)
+    svsa.svsa_sync_status()

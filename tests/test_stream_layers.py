@@ -12,8 +12,8 @@ class _Stream:
     """Stands in for torch.cuda.Stream (and, called, for torch.cuda.stream)."""
     current = None
 
-    def __init__(self, name):
-        self.name, self.cuda_stream = name, 0
+    def __init__(self, name, device="cpu"):
+        self.name, self.device, self.cuda_stream = name, torch.device(device), 0
 
 
 @pytest.fixture
@@ -77,6 +77,16 @@ def test_a_call_on_a_stream_does_all_its_work_there(streams, name):
         del log[:]
     call(None)
     assert log and all(now is None and given is None for _, now, given in log)
+
+
+@pytest.mark.parametrize("name", ["append", "reset", "select", "attend", "norm", "gradients"])
+def test_a_stream_of_another_device_is_refused(streams, name):
+    _, log = streams
+    call = _calls()[name]
+    del log[:]
+    with pytest.raises(ValueError, match="stream"):
+        call(_Stream("c", "cuda:1"))
+    assert not log and _Stream.current is None
 
 
 def test_norm_and_rotation_record_their_gradients(monkeypatch):
